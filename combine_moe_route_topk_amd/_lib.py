@@ -43,6 +43,10 @@ SIGNATURES = {
     "moe_scatter_rows": (ctypes.c_int, [_p, _i64, _i64, _i32, _p, _p, _p]),
     "moe_gather_rows": (ctypes.c_int, [_p, _i64, _i64, _i32, _p, _i64, _p, _p]),
     "moe_combine": (ctypes.c_int, [_p, _i32, _i64, _i64, _i32, _p, _p, _p, _i32, _p]),
+    "moe_combine_backward": (ctypes.c_int, [_p, _i32, _p, _i32, _i64, _i64, _i32, _p, _p, _p, _p,
+                                            _p]),
+    "moe_dispatch_backward": (ctypes.c_int, [_p, _i32, _i64, _i64, _i32, _p, _p, _i32, _p]),
+    "moe_route_topk_backward": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i32, _i32, _i32, _p, _p]),
     "moe_dequant_rows": (ctypes.c_int, [_p, _p, _i64, _i64, _p, _p]),
     "moe_grouped_swiglu_workspace_bytes": (_sz, [_i64, _i32, _i64, _i64]),
     "moe_grouped_swiglu": (ctypes.c_int, [_p, _i64, _i64, _p, _i32, _p, _p, _p, _i64, _p, _p,

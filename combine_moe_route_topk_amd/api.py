@@ -17,7 +17,8 @@ import torch
 from ._lib import (MOE_BF16, MOE_F32, MOE_F8E4M3, MOE_SORT_AUTO, MoeError, check, lib)
 
 __all__ = ["moe_route_topk", "moe_resolve_sorted", "default_sort_cutoff", "moe_dispatch_workspace_bytes", "moe_dispatch",
-           "moe_combine", "moe_dequant_rows", "moe_scatter_rows", "moe_gather_rows",
+           "moe_combine", "moe_combine_backward", "moe_dispatch_backward", "moe_route_topk_backward",
+           "moe_dequant_rows", "moe_scatter_rows", "moe_gather_rows",
            "moe_route_dispatch", "moe_route_dispatch_noalloc", "moe_route_dispatch_workspace_bytes", "moe_grouped_swiglu_workspace_bytes",
            "moe_grouped_swiglu", "moe_grouped_gemm_fp8", "moe_gather_swiglu_workspace_bytes",
            "moe_gather_swiglu", "moe_gather_swiglu_combine", "moe_abi_version", "DispatchResult",
@@ -32,6 +33,26 @@ def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _launch(fn: str, dev: torch.device, stream, args, own=()) -> None:
+    """Call C function `fn` with its stream on the operands' device, whichever
+    device and stream are current.  `own`: tensors allocated in the call; on
+    another stream than the current one their memory must not be handed out
+    again before that stream has passed the call."""
+    cur = torch.cuda.current_stream(dev)
+    if stream is None:
+        stream = cur
+    elif stream.device != dev:
+        raise ValueError(f"{fn}: the stream is on {stream.device}, the operands on {dev}")
+    if dev.index == torch.cuda.current_device():
+        check(fn, getattr(lib, fn)(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            check(fn, getattr(lib, fn)(*args, _stream(stream)))
+    if stream != cur:
+        for t in own:
+            t.record_stream(stream)
 
 
 def _need(t: torch.Tensor, name: str, dtypes, device=None) -> None:
@@ -351,6 +372,97 @@ def moe_combine(y: torch.Tensor, dst_pos: torch.Tensor, topk_w: torch.Tensor,
                                          _ptr(topk_w), _ptr(out), _FLOAT_IO[out.dtype],
                                          _stream(stream)))
     return out
+
+
+def moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, dst_pos: torch.Tensor,
+                         topk_w: torch.Tensor, d_y: Optional[torch.Tensor] = None,
+                         d_topk_w: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of moe_combine: d_out [N, D] float32/bfloat16 and the forward
+    call's y [N*k, D], dst_pos, topk_w [N, k] -> (d_y [N*k, D] of y's dtype,
+    d_topk_w [N, k] float32).  Rows of d_y that no pair names (dropped pairs,
+    dst_pos outside [0, N*k)) keep what d_y held: pass a zeroed d_y then."""
+    _need(y, "y", tuple(_FLOAT_IO))
+    dev = y.device
+    _need(d_out, "d_out", tuple(_FLOAT_IO), dev)
+    _need(dst_pos, "dst_pos", (torch.int32,), dev)
+    _need(topk_w, "topk_w", (torch.float32,), dev)
+    if topk_w.dim() != 2 or y.dim() != 2:
+        raise ValueError("topk_w must be [N, k] and y [N*k, D]")
+    n, k = topk_w.shape
+    hidden = y.shape[1]
+    _shape(d_out, "d_out", (n, hidden))
+    if dst_pos.numel() != n * k or y.shape[0] != n * k:
+        raise ValueError("y / dst_pos must hold N*k rows")
+    own = []
+    if d_y is None:
+        d_y = torch.empty_like(y)
+        own.append(d_y)
+    if d_topk_w is None:
+        d_topk_w = torch.empty_like(topk_w)
+        own.append(d_topk_w)
+    _need(d_y, "d_y", (y.dtype,), dev)
+    _shape(d_y, "d_y", y.shape)
+    _need(d_topk_w, "d_topk_w", (torch.float32,), dev)
+    _shape(d_topk_w, "d_topk_w", (n, k))
+    _launch("moe_combine_backward", dev, stream,
+            (_ptr(d_out), _FLOAT_IO[d_out.dtype], _ptr(y), _FLOAT_IO[y.dtype], n, hidden, k,
+             _ptr(dst_pos), _ptr(topk_w), _ptr(d_y), _ptr(d_topk_w)), own)
+    return d_y, d_topk_w
+
+
+def moe_dispatch_backward(d_rows: torch.Tensor, dst_pos: torch.Tensor, k: int,
+                          out_dtype: Optional[torch.dtype] = None,
+                          d_x: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of moe_dispatch's rows: d_rows [N*k, D] float32/bfloat16,
+    dst_pos [N*k] -> d_x [N, D], d_x[t] = sum_j d_rows[dst_pos[t*k+j]]."""
+    _need(d_rows, "d_rows", tuple(_FLOAT_IO))
+    dev = d_rows.device
+    _need(dst_pos, "dst_pos", (torch.int32,), dev)
+    if d_rows.dim() != 2 or k < 1 or d_rows.shape[0] % k or dst_pos.numel() != d_rows.shape[0]:
+        raise ValueError("d_rows must be [N*k, D] and dst_pos must hold N*k entries")
+    n, hidden = d_rows.shape[0] // k, d_rows.shape[1]
+    own = []
+    if d_x is None:
+        d_x = torch.empty((n, hidden), dtype=out_dtype or d_rows.dtype, device=dev)
+        own.append(d_x)
+    _need(d_x, "d_x", tuple(_FLOAT_IO), dev)
+    _shape(d_x, "d_x", (n, hidden))
+    _launch("moe_dispatch_backward", dev, stream,
+            (_ptr(d_rows), _FLOAT_IO[d_rows.dtype], n, hidden, k, _ptr(dst_pos), _ptr(d_x),
+             _FLOAT_IO[d_x.dtype]), own)
+    return d_x
+
+
+def moe_route_topk_backward(topk_idx: torch.Tensor, topk_w: torch.Tensor, d_topk_w: torch.Tensor,
+                            n_experts: int, renormalize: bool = True,
+                            logits: Optional[torch.Tensor] = None,
+                            d_logits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of moe_route_topk's weights: topk_idx, topk_w [N, k] of the
+    forward call (same renormalize) and d_topk_w [N, k] -> d_logits [N, E]
+    float32.  logits [N, E] are needed only with renormalize=False."""
+    _need(topk_idx, "topk_idx", (torch.int32,))
+    dev = topk_idx.device
+    if topk_idx.dim() != 2:
+        raise ValueError("topk_idx must be [N, k]")
+    n, k = topk_idx.shape
+    for name, t in (("topk_w", topk_w), ("d_topk_w", d_topk_w)):
+        _need(t, name, (torch.float32,), dev)
+        _shape(t, name, (n, k))
+    if logits is not None:
+        _need(logits, "logits", (torch.float32,), dev)
+        _shape(logits, "logits", (n, n_experts))
+    elif not renormalize:
+        raise ValueError("renormalize=False needs the logits")
+    own = []
+    if d_logits is None:
+        d_logits = torch.empty((n, n_experts), dtype=torch.float32, device=dev)
+        own.append(d_logits)
+    _need(d_logits, "d_logits", (torch.float32,), dev)
+    _shape(d_logits, "d_logits", (n, n_experts))
+    _launch("moe_route_topk_backward", dev, stream,
+            (_ptr(logits), _ptr(topk_idx), _ptr(topk_w), _ptr(d_topk_w), n, n_experts, k,
+             int(bool(renormalize)), _ptr(d_logits)), own)
+    return d_logits
 
 
 def moe_dequant_rows(rows: torch.Tensor, row_scales: torch.Tensor,

@@ -377,6 +377,78 @@ int moe_combine(const void* y, int32_t y_dtype, int64_t n_tokens, int64_t hidden
                     fn);
 }
 
+namespace {
+// sizes of the [NK, D] row gradients and the alignment of their elements
+int check_row_gradient(const char* fn, int64_t n_tokens, int64_t hidden, int32_t k, int32_t dt_a,
+                       int32_t dt_b) {
+  if (n_tokens < 0) return fail(MOE_ERR_ARG, "%s: n_tokens < 0", fn);
+  if (hidden < 1) return fail(MOE_ERR_ARG, "%s: hidden < 1", fn);
+  if (k < 1) return fail(MOE_ERR_ARG, "%s: k < 1", fn);
+  if ((dt_a != MOE_F32 && dt_a != MOE_BF16) || (dt_b != MOE_F32 && dt_b != MOE_BF16))
+    return fail(MOE_ERR_ARG, "%s: dtypes must be MOE_F32 or MOE_BF16", fn);
+  if (k > MOE_MAX_TOPK) return fail(MOE_ERR_UNSUPPORTED, "%s: k > %d", fn, MOE_MAX_TOPK);
+  if (n_tokens > INT32_MAX / k)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: n_tokens * k exceeds the int32 index range", fn);
+  return MOE_OK;
+}
+bool misaligned(const void* p, int32_t dtype) {
+  return reinterpret_cast<uintptr_t>(p) & (dtype == MOE_F32 ? 3 : 1);
+}
+bool misaligned4(const void* p) { return reinterpret_cast<uintptr_t>(p) & 3; }
+}  // namespace
+
+int moe_combine_backward(const void* d_out, int32_t g_dtype, const void* y, int32_t y_dtype,
+                         int64_t n_tokens, int64_t hidden, int32_t k, const int32_t* dst_pos,
+                         const float* topk_w, void* d_y, float* d_topk_w, void* stream) {
+  const char* fn = "moe_combine_backward";
+  const int rc = check_row_gradient(fn, n_tokens, hidden, k, g_dtype, y_dtype);
+  if (rc) return rc;
+  if (n_tokens == 0) return ok();
+  if (!d_out || !y || !dst_pos || !topk_w || !d_y || !d_topk_w)
+    return fail(MOE_ERR_ARG, "%s: null pointer argument", fn);
+  if (misaligned(d_out, g_dtype) || misaligned(y, y_dtype) || misaligned(d_y, y_dtype) ||
+      misaligned4(dst_pos) || misaligned4(topk_w) || misaligned4(d_topk_w))
+    return fail(MOE_ERR_ARG, "%s: pointers must be aligned to their elements", fn);
+  return hip_status(moe::launch_combine_backward(d_out, g_dtype == MOE_BF16, y, y_dtype == MOE_BF16,
+                                                 n_tokens, hidden, k, dst_pos, topk_w, d_y,
+                                                 d_topk_w, static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+int moe_dispatch_backward(const void* d_rows, int32_t rows_dtype, int64_t n_tokens, int64_t hidden,
+                          int32_t k, const int32_t* dst_pos, void* d_x, int32_t x_dtype,
+                          void* stream) {
+  const char* fn = "moe_dispatch_backward";
+  const int rc = check_row_gradient(fn, n_tokens, hidden, k, rows_dtype, x_dtype);
+  if (rc) return rc;
+  if (n_tokens == 0) return ok();
+  if (!d_rows || !dst_pos || !d_x) return fail(MOE_ERR_ARG, "%s: null pointer argument", fn);
+  if (misaligned(d_rows, rows_dtype) || misaligned(d_x, x_dtype) || misaligned4(dst_pos))
+    return fail(MOE_ERR_ARG, "%s: pointers must be aligned to their elements", fn);
+  return hip_status(moe::launch_dispatch_backward(d_rows, rows_dtype == MOE_BF16, n_tokens, hidden,
+                                                  k, dst_pos, d_x, x_dtype == MOE_BF16,
+                                                  static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+int moe_route_topk_backward(const float* logits, const int32_t* topk_idx, const float* topk_w,
+                            const float* d_topk_w, int64_t n_tokens, int32_t n_experts, int32_t k,
+                            int32_t renormalize, float* d_logits, void* stream) {
+  const char* fn = "moe_route_topk_backward";
+  const int rc = check_routing_sizes(fn, n_tokens, n_experts, k);
+  if (rc) return rc;
+  if (n_tokens == 0) return ok();
+  if (!topk_idx || !topk_w || !d_topk_w || !d_logits || (!renormalize && !logits))
+    return fail(MOE_ERR_ARG, "%s: null pointer argument", fn);
+  if (misaligned4(logits) || misaligned4(topk_idx) || misaligned4(topk_w) ||
+      misaligned4(d_topk_w) || misaligned4(d_logits))
+    return fail(MOE_ERR_ARG, "%s: pointers must be aligned to their elements", fn);
+  return hip_status(moe::launch_route_topk_backward(logits, topk_idx, topk_w, d_topk_w, n_tokens,
+                                                    n_experts, k, renormalize ? 1 : 0, d_logits,
+                                                    static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
 int moe_dequant_rows(const uint8_t* rows, const float* row_scales, int64_t n_rows, int64_t hidden,
                      uint16_t* y, void* stream) {
   const char* fn = "moe_dequant_rows";

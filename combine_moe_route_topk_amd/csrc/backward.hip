@@ -1,0 +1,272 @@
+// Gradients of the combine and of the routing weights.
+//
+// Combine:  out[t] = sum_j w[t, j] y[p],  p = dst_pos[t*k + j]
+//   d_y[p]    = w[t, j] d_out[t]          (rounded once to y's type)
+//   d_w[t, j] = sum_i d_out[t, i] y[p, i]
+// Routing weights, S = sum_j w_j d_j over a token's slots (d = d_topk_w):
+//   renormalised over the selected experts: d_logits[idx_j] = w_j (d_j - S), else 0
+//   full softmax p:  d_logits[e] = sum_{j: idx_j = e} w_j d_j - p_e S
+// The dispatch's gradient is the combine with unit weights (combine.hip).
+#include "device_common.hpp"
+#include "launch.hpp"
+
+namespace moe {
+
+namespace {
+
+constexpr int kBlock = 256;
+constexpr int kWaves = kBlock / kWave;
+constexpr int kGroup = 8;          // elements per lane per load group
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// Sum over the wave, the same in every lane (a fixed order of additions).
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// 8 consecutive elements of a row in registers as loaded.
+template <typename T> struct Raw;
+template <> struct Raw<uint16_t> {
+  u32x4 v;
+  template <bool NT> __device__ void load(const uint16_t* p) {
+    v = NT ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p))
+           : *reinterpret_cast<const u32x4*>(p);
+  }
+  __device__ void to_f32(float (&o)[kGroup]) const {
+    unpack_bf16x2(v.x, o[0], o[1]); unpack_bf16x2(v.y, o[2], o[3]);
+    unpack_bf16x2(v.z, o[4], o[5]); unpack_bf16x2(v.w, o[6], o[7]);
+  }
+  __device__ static uint32_t pack(float a, float b) {   // rounds to nearest even
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+  }
+  __device__ static void store(uint16_t* p, const float (&o)[kGroup]) {
+    const u32x4 r = {pack(o[0], o[1]), pack(o[2], o[3]), pack(o[4], o[5]), pack(o[6], o[7])};
+    __builtin_nontemporal_store(r, reinterpret_cast<u32x4*>(p));
+  }
+};
+template <> struct Raw<float> {
+  u32x4 a, b;
+  template <bool NT> __device__ void load(const float* p) {
+    const u32x4* q = reinterpret_cast<const u32x4*>(p);
+    a = NT ? __builtin_nontemporal_load(q) : q[0];
+    b = NT ? __builtin_nontemporal_load(q + 1) : q[1];
+  }
+  __device__ void to_f32(float (&o)[kGroup]) const {
+    o[0] = __uint_as_float(a.x); o[1] = __uint_as_float(a.y);
+    o[2] = __uint_as_float(a.z); o[3] = __uint_as_float(a.w);
+    o[4] = __uint_as_float(b.x); o[5] = __uint_as_float(b.y);
+    o[6] = __uint_as_float(b.z); o[7] = __uint_as_float(b.w);
+  }
+  __device__ static void store(float* p, const float (&o)[kGroup]) {
+    u32x4* q = reinterpret_cast<u32x4*>(p);
+    __builtin_nontemporal_store(u32x4{__float_as_uint(o[0]), __float_as_uint(o[1]),
+                                      __float_as_uint(o[2]), __float_as_uint(o[3])}, q);
+    __builtin_nontemporal_store(u32x4{__float_as_uint(o[4]), __float_as_uint(o[5]),
+                                      __float_as_uint(o[6]), __float_as_uint(o[7])}, q + 1);
+  }
+};
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store1(uint16_t* p, float v) { *p = f32_to_bf16_rne(v); }
+
+// One wave per pair q = t*k + j: it reads row dst_pos[q] of y and row t of
+// d_out once, writes row dst_pos[q] of d_y, and keeps the dot product in fp32
+// registers, so d_w needs no second pass, no atomics and no workspace.  The k
+// waves of a token sit side by side, so d_out comes from the caches after the
+// first.  y and d_y are touched once and bypass them (non-temporal).
+template <typename TG, typename TY, int U>
+__global__ __launch_bounds__(kBlock) void combine_backward_kernel(
+    const TG* __restrict__ d_out, const TY* __restrict__ y, int64_t nk, int64_t hidden, int k,
+    const int32_t* __restrict__ dst_pos, const float* __restrict__ topk_w, TY* __restrict__ d_y,
+    float* __restrict__ d_w) {
+  const int lane = lane_id();
+  const int64_t q = int64_t(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(int(threadIdx.x / kWave));
+  if (q >= nk) return;
+  const int p = __builtin_amdgcn_readfirstlane(dst_pos[q]);
+  if (unsigned(p) >= uint64_t(nk)) {            // a pair that holds no row
+    if (lane == 0) d_w[q] = 0.f;
+    return;
+  }
+  const float w = topk_w[q];
+  const TG* g = d_out + q / k * hidden;
+  const TY* yr = y + int64_t(p) * hidden;
+  TY* dr = d_y + int64_t(p) * hidden;
+  float dot = 0.f;
+  const int64_t ngroups = hidden / kGroup;
+  for (int64_t g0 = lane; g0 < ngroups; g0 += U * kWave) {
+    Raw<TG> rg[U];
+    Raw<TY> ry[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // past the row's end: its last group again, not used
+      const int64_t gi = g0 + u * kWave < ngroups ? g0 + u * kWave : ngroups - 1;
+      ry[u].template load<true>(yr + gi * kGroup);
+      rg[u].template load<false>(g + gi * kGroup);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (g0 + u * kWave >= ngroups) break;
+      float a[kGroup], b[kGroup];
+      rg[u].to_f32(a);
+      ry[u].to_f32(b);
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        dot = __builtin_fmaf(a[i], b[i], dot);
+        a[i] *= w;
+      }
+      Raw<TY>::store(dr + (g0 + u * kWave) * kGroup, a);
+    }
+  }
+  dot = wave_sum(dot);
+  if (lane == 0) d_w[q] = dot;
+}
+
+// Any D and alignment: one element per lane.
+template <typename TG, typename TY>
+__global__ __launch_bounds__(kBlock) void combine_backward_scalar_kernel(
+    const TG* __restrict__ d_out, const TY* __restrict__ y, int64_t nk, int64_t hidden, int k,
+    const int32_t* __restrict__ dst_pos, const float* __restrict__ topk_w, TY* __restrict__ d_y,
+    float* __restrict__ d_w) {
+  const int lane = lane_id();
+  const int64_t q = int64_t(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(int(threadIdx.x / kWave));
+  if (q >= nk) return;
+  const int p = __builtin_amdgcn_readfirstlane(dst_pos[q]);
+  if (unsigned(p) >= uint64_t(nk)) {
+    if (lane == 0) d_w[q] = 0.f;
+    return;
+  }
+  const float w = topk_w[q];
+  const TG* g = d_out + q / k * hidden;
+  const TY* yr = y + int64_t(p) * hidden;
+  TY* dr = d_y + int64_t(p) * hidden;
+  float dot = 0.f;
+  for (int64_t i = lane; i < hidden; i += kWave) {
+    const float a = load1(g + i);
+    dot = __builtin_fmaf(a, load1(yr + i), dot);
+    store1(dr + i, w * a);
+  }
+  dot = wave_sum(dot);
+  if (lane == 0) d_w[q] = dot;
+}
+
+template <typename TG, typename TY>
+hipError_t launch_combine_backward_typed(const void* d_out, const void* y, int64_t n_tokens,
+                                         int64_t hidden, int k, const int32_t* dst_pos,
+                                         const float* topk_w, void* d_y, float* d_w,
+                                         hipStream_t stream) {
+  const int64_t nk = n_tokens * k;
+  const unsigned blocks = unsigned((nk + kWaves - 1) / kWaves);
+  const bool aligned = ((reinterpret_cast<uintptr_t>(d_out) | reinterpret_cast<uintptr_t>(y) |
+                         reinterpret_cast<uintptr_t>(d_y)) & 15) == 0;
+  const TG* g = static_cast<const TG*>(d_out);
+  const TY* yy = static_cast<const TY*>(y);
+  TY* dy = static_cast<TY*>(d_y);
+  if (aligned && hidden % kGroup == 0)
+    combine_backward_kernel<TG, TY, 4><<<blocks, kBlock, 0, stream>>>(g, yy, nk, hidden, k, dst_pos,
+                                                                      topk_w, dy, d_w);
+  else
+    combine_backward_scalar_kernel<TG, TY><<<blocks, kBlock, 0, stream>>>(g, yy, nk, hidden, k,
+                                                                          dst_pos, topk_w, dy, d_w);
+  return hipGetLastError();
+}
+
+// One wave per token; lane l holds experts l, l + 64, ..., so a row is written
+// in whole 256-byte runs.  The slots are added in order j = 0..k-1, also where
+// two of them name the same expert.  RENORM false needs the full softmax
+// again: p_e = exp(l_e - l_r) w_r with r the first slot's expert, the largest
+// logit, whose weight w_r is 1 / sum exp(l - l_r); no pass for the sum.
+template <int SLOTS, bool RENORM>
+__global__ __launch_bounds__(kBlock) void route_backward_kernel(
+    const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
+    const float* __restrict__ topk_w, const float* __restrict__ d_w, int64_t n_tokens,
+    int n_experts, int k, float* __restrict__ d_logits) {
+  const int lane = lane_id();
+  const int64_t t = int64_t(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(int(threadIdx.x / kWave));
+  if (t >= n_tokens) return;
+  const bool has = lane < k;
+  const int my_e = has ? topk_idx[t * k + lane] : -1;
+  const bool ok = unsigned(my_e) < unsigned(n_experts);
+  const float w = ok ? topk_w[t * k + lane] : 0.f;
+  const float wd = ok ? w * d_w[t * k + lane] : 0.f;
+  float l[SLOTS], l_r = 0.f, w_r = 0.f;
+  if (!RENORM) {
+    const int e_r = __builtin_amdgcn_readfirstlane(my_e);
+    if (unsigned(e_r) < unsigned(n_experts)) {
+      l_r = logits[t * n_experts + e_r];
+      w_r = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(w)));
+    }
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      const int e = s * kWave + lane;
+      l[s] = e < n_experts ? logits[t * n_experts + e] : 0.f;
+    }
+  }
+  float sum = 0.f;
+  for (int j = 0; j < k; ++j) sum += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wd), j));
+  const float mine = RENORM ? wd - w * sum : wd;
+  float d[SLOTS];
+#pragma unroll
+  for (int s = 0; s < SLOTS; ++s) d[s] = RENORM ? 0.f : -(expf(l[s] - l_r) * w_r) * sum;
+  for (int j = 0; j < k; ++j) {
+    const int e = __builtin_amdgcn_readlane(my_e, j);
+    const float v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), j));
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) d[s] += e == s * kWave + lane ? v : 0.f;
+  }
+#pragma unroll
+  for (int s = 0; s < SLOTS; ++s) {
+    const int e = s * kWave + lane;
+    if (e < n_experts) d_logits[t * n_experts + e] = d[s];
+  }
+}
+
+template <bool RENORM>
+void launch_route_backward_slots(const float* logits, const int32_t* idx, const float* w,
+                                 const float* d_w, int64_t n, int e, int k, float* d_logits,
+                                 hipStream_t stream) {
+  const unsigned blocks = unsigned((n + kWaves - 1) / kWaves);
+  if (e <= 64)
+    route_backward_kernel<1, RENORM><<<blocks, kBlock, 0, stream>>>(logits, idx, w, d_w, n, e, k, d_logits);
+  else if (e <= 128)
+    route_backward_kernel<2, RENORM><<<blocks, kBlock, 0, stream>>>(logits, idx, w, d_w, n, e, k, d_logits);
+  else if (e <= 256)
+    route_backward_kernel<4, RENORM><<<blocks, kBlock, 0, stream>>>(logits, idx, w, d_w, n, e, k, d_logits);
+  else if (e <= 512)
+    route_backward_kernel<8, RENORM><<<blocks, kBlock, 0, stream>>>(logits, idx, w, d_w, n, e, k, d_logits);
+  else
+    route_backward_kernel<16, RENORM><<<blocks, kBlock, 0, stream>>>(logits, idx, w, d_w, n, e, k, d_logits);
+}
+
+}  // namespace
+
+hipError_t launch_combine_backward(const void* d_out, int g_bf16, const void* y, int y_bf16,
+                                   int64_t n_tokens, int64_t hidden, int k, const int32_t* dst_pos,
+                                   const float* topk_w, void* d_y, float* d_topk_w,
+                                   hipStream_t stream) {
+  if (g_bf16 && y_bf16)
+    return launch_combine_backward_typed<uint16_t, uint16_t>(d_out, y, n_tokens, hidden, k, dst_pos, topk_w, d_y, d_topk_w, stream);
+  if (g_bf16)
+    return launch_combine_backward_typed<uint16_t, float>(d_out, y, n_tokens, hidden, k, dst_pos, topk_w, d_y, d_topk_w, stream);
+  if (y_bf16)
+    return launch_combine_backward_typed<float, uint16_t>(d_out, y, n_tokens, hidden, k, dst_pos, topk_w, d_y, d_topk_w, stream);
+  return launch_combine_backward_typed<float, float>(d_out, y, n_tokens, hidden, k, dst_pos, topk_w, d_y, d_topk_w, stream);
+}
+
+hipError_t launch_route_topk_backward(const float* logits, const int32_t* topk_idx,
+                                      const float* topk_w, const float* d_topk_w,
+                                      int64_t n_tokens, int n_experts, int k, int renormalize,
+                                      float* d_logits, hipStream_t stream) {
+  if (renormalize)
+    launch_route_backward_slots<true>(logits, topk_idx, topk_w, d_topk_w, n_tokens, n_experts, k, d_logits, stream);
+  else
+    launch_route_backward_slots<false>(logits, topk_idx, topk_w, d_topk_w, n_tokens, n_experts, k, d_logits, stream);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -99,7 +99,8 @@ template <> struct Raw<float> {
   }
 };
 
-template <typename TY, typename TO, int U, int KB>
+// W false: every weight is 1 and topk_w is not read (the dispatch's gradient).
+template <typename TY, typename TO, int U, int KB, bool W>
 __global__ __launch_bounds__(kBlock) void combine_kernel(const TY* __restrict__ y, int64_t n_tokens,
                                                          int64_t hidden, int k, int n_slices,
                                                          const int32_t* __restrict__ dst_pos,
@@ -128,7 +129,7 @@ __global__ __launch_bounds__(kBlock) void combine_kernel(const TY* __restrict__ 
 
   // lane j < k holds slot j's position and weight; slots are read with readlane
   const int my_p = lane < k ? dst_pos[t * k + lane] : -1;
-  const float my_w = lane < k ? topk_w[t * k + lane] : 0.f;
+  const float my_w = W && lane < k ? topk_w[t * k + lane] : 0.f;
   for (int j0 = 0; j0 < k; j0 += KB) {
     Raw<TY> raw[KB][U];
     const TY* row[KB];
@@ -138,7 +139,7 @@ __global__ __launch_bounds__(kBlock) void combine_kernel(const TY* __restrict__ 
     for (int jj = 0; jj < KB; ++jj) {
       const int p = __builtin_amdgcn_readlane(my_p, j0 + jj);   // -1 past the last slot
       use[jj] = unsigned(p) < uint64_t(nk);
-      wj[jj] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, my_w), j0 + jj));
+      wj[jj] = W ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, my_w), j0 + jj)) : 1.f;
       row[jj] = y + int64_t(use[jj] ? p : 0) * hidden;
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -168,7 +169,7 @@ __global__ __launch_bounds__(kBlock) void combine_kernel(const TY* __restrict__ 
 }
 
 // Scalar path for any D: one element per lane, a slice is 64 elements.
-template <typename TY, typename TO>
+template <typename TY, typename TO, bool W>
 __global__ __launch_bounds__(kBlock) void combine_scalar_kernel(
     const TY* __restrict__ y, int64_t n_tokens, int64_t hidden, int k, int n_slices,
     const int32_t* __restrict__ dst_pos, const float* __restrict__ topk_w, int64_t nk,
@@ -184,12 +185,12 @@ __global__ __launch_bounds__(kBlock) void combine_scalar_kernel(
   for (int j = 0; j < k; ++j) {
     const int p = dst_pos[t * k + j];
     if (unsigned(p) >= uint64_t(nk)) continue;
-    acc = __builtin_fmaf(topk_w[t * k + j], Elem<TY>::load1(y + int64_t(p) * hidden, i), acc);
+    acc = __builtin_fmaf(W ? topk_w[t * k + j] : 1.f, Elem<TY>::load1(y + int64_t(p) * hidden, i), acc);
   }
   Elem<TO>::store1(out + t * hidden, i, acc);
 }
 
-template <typename TY, typename TO>
+template <typename TY, typename TO, bool W>
 hipError_t launch_combine_typed(const void* y, int64_t n_tokens, int64_t hidden, int k,
                                 const int32_t* dst_pos, const float* topk_w, void* out,
                                 hipStream_t stream) {
@@ -207,13 +208,13 @@ hipError_t launch_combine_typed(const void* y, int64_t n_tokens, int64_t hidden,
     const TY* yy = static_cast<const TY*>(y);
     TO* oo = static_cast<TO*>(out);
     if (k >= 8)
-      combine_kernel<TY, TO, U, 8><<<blocks, kBlock, 0, stream>>>(yy, n_tokens, hidden, k, n_slices, dst_pos, topk_w, nk, oo);
+      combine_kernel<TY, TO, U, 8, W><<<blocks, kBlock, 0, stream>>>(yy, n_tokens, hidden, k, n_slices, dst_pos, topk_w, nk, oo);
     else if (k >= 4)
-      combine_kernel<TY, TO, U, 4><<<blocks, kBlock, 0, stream>>>(yy, n_tokens, hidden, k, n_slices, dst_pos, topk_w, nk, oo);
+      combine_kernel<TY, TO, U, 4, W><<<blocks, kBlock, 0, stream>>>(yy, n_tokens, hidden, k, n_slices, dst_pos, topk_w, nk, oo);
     else if (k >= 2)
-      combine_kernel<TY, TO, U, 2><<<blocks, kBlock, 0, stream>>>(yy, n_tokens, hidden, k, n_slices, dst_pos, topk_w, nk, oo);
+      combine_kernel<TY, TO, U, 2, W><<<blocks, kBlock, 0, stream>>>(yy, n_tokens, hidden, k, n_slices, dst_pos, topk_w, nk, oo);
     else
-      combine_kernel<TY, TO, U, 1><<<blocks, kBlock, 0, stream>>>(yy, n_tokens, hidden, k, n_slices, dst_pos, topk_w, nk, oo);
+      combine_kernel<TY, TO, U, 1, W><<<blocks, kBlock, 0, stream>>>(yy, n_tokens, hidden, k, n_slices, dst_pos, topk_w, nk, oo);
   } else if (hidden % kGroup == 0 && aligned) {
     constexpr int U = 2;
     const int64_t ngroups = hidden / kGroup;
@@ -223,17 +224,17 @@ hipError_t launch_combine_typed(const void* y, int64_t n_tokens, int64_t hidden,
     const TY* yy = static_cast<const TY*>(y);
     TO* oo = static_cast<TO*>(out);
     if (k >= 8)
-      combine_kernel<TY, TO, U, 8><<<blocks, kBlock, 0, stream>>>(yy, n_tokens, hidden, k, n_slices, dst_pos, topk_w, nk, oo);
+      combine_kernel<TY, TO, U, 8, W><<<blocks, kBlock, 0, stream>>>(yy, n_tokens, hidden, k, n_slices, dst_pos, topk_w, nk, oo);
     else if (k >= 4)
-      combine_kernel<TY, TO, U, 4><<<blocks, kBlock, 0, stream>>>(yy, n_tokens, hidden, k, n_slices, dst_pos, topk_w, nk, oo);
+      combine_kernel<TY, TO, U, 4, W><<<blocks, kBlock, 0, stream>>>(yy, n_tokens, hidden, k, n_slices, dst_pos, topk_w, nk, oo);
     else if (k >= 2)
-      combine_kernel<TY, TO, U, 2><<<blocks, kBlock, 0, stream>>>(yy, n_tokens, hidden, k, n_slices, dst_pos, topk_w, nk, oo);
+      combine_kernel<TY, TO, U, 2, W><<<blocks, kBlock, 0, stream>>>(yy, n_tokens, hidden, k, n_slices, dst_pos, topk_w, nk, oo);
     else
-      combine_kernel<TY, TO, U, 1><<<blocks, kBlock, 0, stream>>>(yy, n_tokens, hidden, k, n_slices, dst_pos, topk_w, nk, oo);
+      combine_kernel<TY, TO, U, 1, W><<<blocks, kBlock, 0, stream>>>(yy, n_tokens, hidden, k, n_slices, dst_pos, topk_w, nk, oo);
   } else {
     const int n_slices = int((hidden + kWave - 1) / kWave);
     const int64_t items = n_tokens * n_slices;
-    combine_scalar_kernel<TY, TO><<<unsigned((items + per_block - 1) / per_block), kBlock, 0, stream>>>(
+    combine_scalar_kernel<TY, TO, W><<<unsigned((items + per_block - 1) / per_block), kBlock, 0, stream>>>(
         static_cast<const TY*>(y), n_tokens, hidden, k, n_slices, dst_pos, topk_w, nk,
         static_cast<TO*>(out));
   }
@@ -295,18 +296,36 @@ __global__ __launch_bounds__(kBlock) void dequant_kernel(const uint8_t* __restri
   dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
+template <bool W>
+hipError_t launch_combine_any(const void* y, int y_bf16, int64_t n_tokens, int64_t hidden, int k,
+                              const int32_t* dst_pos, const float* topk_w, void* out, int out_bf16,
+                              hipStream_t stream) {
+  if (y_bf16 && out_bf16)
+    return launch_combine_typed<uint16_t, uint16_t, W>(y, n_tokens, hidden, k, dst_pos, topk_w, out, stream);
+  if (y_bf16)
+    return launch_combine_typed<uint16_t, float, W>(y, n_tokens, hidden, k, dst_pos, topk_w, out, stream);
+  if (out_bf16)
+    return launch_combine_typed<float, uint16_t, W>(y, n_tokens, hidden, k, dst_pos, topk_w, out, stream);
+  return launch_combine_typed<float, float, W>(y, n_tokens, hidden, k, dst_pos, topk_w, out, stream);
+}
+
 }  // namespace
 
 hipError_t launch_combine(const void* y, int y_bf16, int64_t n_tokens, int64_t hidden, int k,
                           const int32_t* dst_pos, const float* topk_w, void* out, int out_bf16,
                           hipStream_t stream) {
-  if (y_bf16 && out_bf16)
-    return launch_combine_typed<uint16_t, uint16_t>(y, n_tokens, hidden, k, dst_pos, topk_w, out, stream);
-  if (y_bf16)
-    return launch_combine_typed<uint16_t, float>(y, n_tokens, hidden, k, dst_pos, topk_w, out, stream);
-  if (out_bf16)
-    return launch_combine_typed<float, uint16_t>(y, n_tokens, hidden, k, dst_pos, topk_w, out, stream);
-  return launch_combine_typed<float, float>(y, n_tokens, hidden, k, dst_pos, topk_w, out, stream);
+  return launch_combine_any<true>(y, y_bf16, n_tokens, hidden, k, dst_pos, topk_w, out, out_bf16,
+                                  stream);
+}
+
+// d_x[t] = sum_j d_rows[dst_pos[t*k + j]]: the combine with every weight 1.
+// Slot order, skipped positions and rounding are the combine's.  Bound by the
+// one pass over d_rows.
+hipError_t launch_dispatch_backward(const void* d_rows, int rows_bf16, int64_t n_tokens,
+                                    int64_t hidden, int k, const int32_t* dst_pos, void* d_x,
+                                    int x_bf16, hipStream_t stream) {
+  return launch_combine_any<false>(d_rows, rows_bf16, n_tokens, hidden, k, dst_pos, nullptr, d_x,
+                                   x_bf16, stream);
 }
 
 hipError_t launch_dequant_rows(const uint8_t* rows, const float* row_scales, int64_t n_rows,

@@ -91,6 +91,19 @@ hipError_t launch_combine(const void* y, int y_bf16, int64_t n_tokens, int64_t h
                           const int32_t* dst_pos, const float* topk_w, void* out, int out_bf16,
                           hipStream_t stream);
 
+// ---- gradients
+hipError_t launch_combine_backward(const void* d_out, int g_bf16, const void* y, int y_bf16,
+                                   int64_t n_tokens, int64_t hidden, int k, const int32_t* dst_pos,
+                                   const float* topk_w, void* d_y, float* d_topk_w,
+                                   hipStream_t stream);
+hipError_t launch_dispatch_backward(const void* d_rows, int rows_bf16, int64_t n_tokens,
+                                    int64_t hidden, int k, const int32_t* dst_pos, void* d_x,
+                                    int x_bf16, hipStream_t stream);
+hipError_t launch_route_topk_backward(const float* logits, const int32_t* topk_idx,
+                                      const float* topk_w, const float* d_topk_w,
+                                      int64_t n_tokens, int n_experts, int k, int renormalize,
+                                      float* d_logits, hipStream_t stream);
+
 // ---- experts
 hipError_t launch_dequant_rows(const uint8_t* rows, const float* row_scales, int64_t n_rows,
                                int64_t hidden, uint16_t* y, hipStream_t stream);

@@ -293,6 +293,59 @@ int moe_combine(const void* y, int32_t y_dtype, int64_t n_tokens, int64_t hidden
                 const int32_t* dst_pos, const float* topk_w,
                 void* out, int32_t out_dtype, void* stream);
 
+/* ---------------------------------------------------------------- gradients
+ * The gradients of the three steps of the token path.  Each takes what its
+ * forward call took or returned, sums in fp32 in a fixed order (the same
+ * result on every call) and needs no workspace.  In-range entries of dst_pos
+ * are distinct, as moe_dispatch writes them; where two pairs name one row,
+ * that row of d_y is unspecified.
+ *
+ * moe_combine_backward -- gradient of moe_combine:
+ *   d_y[dst_pos[q], i] = topk_w[q] * d_out[q / k, i]   (rounded once to y_dtype)
+ *   d_topk_w[q]        = sum_i d_out[q / k, i] * y[dst_pos[q], i]
+ * A pair whose position lies outside [0, NK) gets d_topk_w = 0 and writes no
+ * row; rows of d_y that no pair names are left as they were (their gradient
+ * is zero: clear d_y first where pairs were dropped).
+ *   d_out     [N, D] of g_dtype (MOE_F32 or MOE_BF16)
+ *   y         [NK, D] of y_dtype (MOE_F32 or MOE_BF16), as given to moe_combine
+ *   dst_pos   [NK] int32, topk_w [N, k] float32
+ *   d_y       [NK, D] of y_dtype, output;  d_topk_w [N, k] float32, output
+ * Errors: MOE_ERR_ARG for null pointers (unless N == 0), N < 0, D < 1,
+ * k < 1, dtypes outside {MOE_F32, MOE_BF16}, or a pointer not aligned to its
+ * elements; MOE_ERR_UNSUPPORTED for k > MOE_MAX_TOPK or NK > INT32_MAX. */
+int moe_combine_backward(const void* d_out, int32_t g_dtype, const void* y, int32_t y_dtype,
+                         int64_t n_tokens, int64_t hidden, int32_t k, const int32_t* dst_pos,
+                         const float* topk_w, void* d_y, float* d_topk_w, void* stream);
+
+/* moe_dispatch_backward -- gradient of moe_dispatch's row copy (and of
+ * moe_scatter_rows):
+ *   d_x[t, i] = sum_{j<k} d_rows[dst_pos[t*k + j], i]
+ * one fp32 sum in slot order, rounded once to x_dtype; entries outside
+ * [0, NK) add nothing (a token with no row left gets zeros).
+ *   d_rows [NK, D] of rows_dtype, dst_pos [NK] int32, d_x [N, D] of x_dtype,
+ *   output; dtypes MOE_F32 or MOE_BF16
+ * Errors: those of moe_combine_backward. */
+int moe_dispatch_backward(const void* d_rows, int32_t rows_dtype, int64_t n_tokens, int64_t hidden,
+                          int32_t k, const int32_t* dst_pos, void* d_x, int32_t x_dtype,
+                          void* stream);
+
+/* moe_route_topk_backward -- gradient of moe_route_topk's weights with respect
+ * to the logits (the selection itself has none).  With
+ * S = sum_j topk_w[t, j] * d_topk_w[t, j]:
+ *   renormalize != 0: d_logits[t, idx_j] = w_j * (d_j - S), 0 elsewhere;
+ *                     logits is not read and may be null
+ *   renormalize == 0: d_logits[t, e] = sum_{j: idx_j = e} w_j * d_j - p_e * S,
+ *                     p the softmax over all E logits.
+ *   logits    [N, E] float32;  topk_idx, topk_w [N, k] from moe_route_topk with
+ *             the same renormalize (slot 0 the largest logit)
+ *   d_topk_w  [N, k] float32;  d_logits [N, E] float32, output (every element)
+ * Slots whose id lies outside [0, E) add nothing.  A row whose logits are all
+ * -inf has NaN weights in the forward call and a NaN gradient here.
+ * Errors: those of moe_route_topk. */
+int moe_route_topk_backward(const float* logits, const int32_t* topk_idx, const float* topk_w,
+                            const float* d_topk_w, int64_t n_tokens, int32_t n_experts, int32_t k,
+                            int32_t renormalize, float* d_logits, void* stream);
+
 /* ---------------------------------------------------------------- experts
  * moe_dequant_rows -- identity expert for an F8 payload: turns dispatched
  * E4M3FN rows and their block scales into bfloat16 rows,
