@@ -21,7 +21,9 @@ __all__ = ["moe_route_topk", "moe_resolve_sorted", "default_sort_cutoff", "moe_d
            "moe_dequant_rows", "moe_scatter_rows", "moe_gather_rows",
            "moe_route_dispatch", "moe_route_dispatch_noalloc", "moe_route_dispatch_workspace_bytes", "moe_grouped_swiglu_workspace_bytes",
            "moe_grouped_swiglu", "moe_grouped_gemm_fp8", "moe_gather_swiglu_workspace_bytes",
-           "moe_gather_swiglu", "moe_gather_swiglu_combine", "moe_abi_version", "DispatchResult",
+           "moe_gather_swiglu", "moe_gather_swiglu_combine", "moe_quantize_mxfp4", "moe_dequant_mxfp4",
+           "moe_grouped_gemm_mxfp4", "moe_gather_gemm_mxfp4", "moe_gather_gemm_mxfp4_workspace_bytes",
+           "moe_abi_version", "DispatchResult",
            "MoeError"]
 
 
@@ -617,4 +619,122 @@ def moe_grouped_gemm_fp8(rows: torch.Tensor, row_scales: torch.Tensor, expert_of
     check("moe_grouped_gemm_fp8", lib.moe_grouped_gemm_fp8(
         _ptr(rows), _ptr(row_scales), r, k, _ptr(expert_offsets), e, _ptr(w), _ptr(w_scales), n,
         _ptr(y), _stream(stream)))
+    return y
+
+
+def _mxfp4_operand(codes: torch.Tensor, scales: torch.Tensor, name: str, dims: int, dev=None) -> None:
+    _need(codes, name, (torch.uint8,), dev)
+    _need(scales, f"{name}'s scales", (torch.uint8,), codes.device)
+    if codes.dim() != dims or codes.shape[-1] % 16:
+        raise ValueError(f"{name} must have {dims} dimensions, the last K/2 with K % 32 == 0")
+    _shape(scales, f"{name}'s scales", tuple(codes.shape[:-1]) + (codes.shape[-1] // 16,))
+
+
+def moe_quantize_mxfp4(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
+                       scales: Optional[torch.Tensor] = None, stream=None):
+    """x [R, K] float32/bfloat16 (K % 32 == 0) -> MXFP4 (codes [R, K/2] uint8,
+    two E2M1 codes per byte, even element low; scales [R, K/32] uint8, E8M0).
+    Weights [E, N, K] are quantised as x.view(E * N, K)."""
+    _need(x, "x", tuple(_FLOAT_IO))
+    dev = x.device
+    if x.dim() != 2 or x.shape[1] % 32:
+        raise ValueError("x must be [R, K] with K % 32 == 0")
+    r, k = x.shape
+    own = []
+    if codes is None:
+        codes = torch.empty((r, k // 2), dtype=torch.uint8, device=dev)
+        own.append(codes)
+    if scales is None:
+        scales = torch.empty((r, k // 32), dtype=torch.uint8, device=dev)
+        own.append(scales)
+    _mxfp4_operand(codes, scales, "codes", 2, dev)
+    _shape(codes, "codes", (r, k // 2))
+    _launch("moe_quantize_mxfp4", dev, stream,
+            (_ptr(x), _FLOAT_IO[x.dtype], r, k, _ptr(codes), _ptr(scales)), own)
+    return codes, scales
+
+
+def moe_dequant_mxfp4(codes: torch.Tensor, scales: torch.Tensor,
+                      out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """MXFP4 codes [R, K/2] and scales [R, K/32] -> their values [R, K]."""
+    _mxfp4_operand(codes, scales, "codes", 2)
+    dev = codes.device
+    r, k = codes.shape[0], codes.shape[1] * 2
+    own = []
+    if out is None:
+        out = torch.empty((r, k), dtype=out_dtype, device=dev)
+        own.append(out)
+    _need(out, "out", tuple(_FLOAT_IO), dev)
+    _shape(out, "out", (r, k))
+    _launch("moe_dequant_mxfp4", dev, stream,
+            (_ptr(codes), _ptr(scales), r, k, _ptr(out), _FLOAT_IO[out.dtype]), own)
+    return out
+
+
+def _mxfp4_product(fn, rows, row_scales, index, n_index, w, w_scales, w_up, w_up_scales, y):
+    """Shared checks of the two MXFP4 products -> (device, sizes, y, own)."""
+    _mxfp4_operand(rows, row_scales, "rows", 2)
+    dev = rows.device
+    _mxfp4_operand(w, w_scales, "w", 3, dev)
+    if (w_up is None) != (w_up_scales is None):
+        raise ValueError(f"{fn}: w_up and w_up_scales go together")
+    if w_up is not None:
+        _mxfp4_operand(w_up, w_up_scales, "w_up", 3, dev)
+        _shape(w_up, "w_up", w.shape)
+    e, n, kh = w.shape
+    if rows.shape[1] != kh:
+        raise ValueError(f"{fn}: rows have {rows.shape[1]} code bytes, w {kh}")
+    _need(index, "expert_offsets / row_expert", (torch.int32,), dev)
+    if index.numel() != (e + 1 if n_index is None else n_index):
+        raise ValueError(f"{fn}: expert_offsets must be [E+1], row_expert [R]")
+    own = []
+    if y is None:
+        y = torch.empty((rows.shape[0], n), dtype=torch.bfloat16, device=dev)
+        own.append(y)
+    _need(y, "y", (torch.bfloat16,), dev)
+    _shape(y, "y", (rows.shape[0], n))
+    return dev, e, n, 2 * kh, y, own
+
+
+def moe_grouped_gemm_mxfp4(rows: torch.Tensor, row_scales: torch.Tensor,
+                           expert_offsets: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                           w_up: Optional[torch.Tensor] = None,
+                           w_up_scales: Optional[torch.Tensor] = None,
+                           y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """MXFP4 rows [R, K/2] with row_scales [R, K/32], grouped by expert through
+    expert_offsets [E+1]; MXFP4 weights w [E, N, K/2] with w_scales [E, N, K/32]
+    -> y [R, N] bf16.  With w_up / w_up_scales (the shapes of w): y =
+    silu(rows w) * (rows w_up).  Rows outside the offsets keep what y held."""
+    dev, e, n, k, y, own = _mxfp4_product("moe_grouped_gemm_mxfp4", rows, row_scales, expert_offsets,
+                                          None, w, w_scales, w_up, w_up_scales, y)
+    _launch("moe_grouped_gemm_mxfp4", dev, stream,
+            (_ptr(rows), _ptr(row_scales), rows.shape[0], k, _ptr(expert_offsets), e, _ptr(w),
+             _ptr(w_scales), _ptr(w_up), _ptr(w_up_scales), n, _ptr(y)), own)
+    return y
+
+
+def moe_gather_gemm_mxfp4_workspace_bytes(n_rows: int, n_experts: int) -> int:
+    return int(lib.moe_gather_gemm_mxfp4_workspace_bytes(n_rows, n_experts))
+
+
+def moe_gather_gemm_mxfp4(rows: torch.Tensor, row_scales: torch.Tensor, row_expert: torch.Tensor,
+                          w: torch.Tensor, w_scales: torch.Tensor,
+                          w_up: Optional[torch.Tensor] = None,
+                          w_up_scales: Optional[torch.Tensor] = None,
+                          y: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """moe_grouped_gemm_mxfp4 over rows in any order, row r taking expert
+    row_expert[r] ([R] int32; rows with an id outside [0, E) keep what y held)."""
+    dev, e, n, k, y, own = _mxfp4_product("moe_gather_gemm_mxfp4", rows, row_scales, row_expert,
+                                          rows.shape[0], w, w_scales, w_up, w_up_scales, y)
+    if workspace is None:
+        workspace = torch.empty(max(moe_gather_gemm_mxfp4_workspace_bytes(rows.shape[0], e), 256),
+                                dtype=torch.uint8, device=dev)
+        own.append(workspace)
+    _need(workspace, "workspace", (torch.uint8,), dev)
+    _launch("moe_gather_gemm_mxfp4", dev, stream,
+            (_ptr(rows), _ptr(row_scales), rows.shape[0], k, _ptr(row_expert), e, _ptr(w),
+             _ptr(w_scales), _ptr(w_up), _ptr(w_up_scales), n, _ptr(y), _ptr(workspace),
+             workspace.numel()), own)
     return y

@@ -616,4 +616,110 @@ int moe_grouped_gemm_fp8(const void* rows, const float* row_scales, int64_t n_ro
                     fn);
 }
 
+namespace {
+bool off(const void* p, unsigned align) { return reinterpret_cast<uintptr_t>(p) & (align - 1); }
+
+int check_mxfp4_rows(const char* fn, int32_t dtype, int64_t n_rows, int64_t k_dim) {
+  if (n_rows < 0) return fail(MOE_ERR_ARG, "%s: n_rows < 0", fn);
+  if (k_dim < 1) return fail(MOE_ERR_ARG, "%s: k_dim < 1", fn);
+  if (dtype != MOE_F32 && dtype != MOE_BF16)
+    return fail(MOE_ERR_ARG, "%s: dtype must be MOE_F32 or MOE_BF16", fn);
+  if (k_dim % 32 != 0) return fail(MOE_ERR_UNSUPPORTED, "%s: k_dim must be a multiple of 32", fn);
+  if (n_rows > (int64_t(1) << 40) / k_dim)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^40 elements", fn);
+  return MOE_OK;
+}
+
+int check_mxfp4_product(const char* fn, const moe::Mxfp4Product& g, const void* index) {
+  if (g.n_rows < 0) return fail(MOE_ERR_ARG, "%s: n_rows < 0", fn);
+  if (g.k_dim < 1 || g.n_dim < 1 || g.n_experts < 1) return fail(MOE_ERR_ARG, "%s: sizes must be >= 1", fn);
+  if (!g.w_up != !g.w_up_scales)
+    return fail(MOE_ERR_ARG, "%s: w_up and w_up_scales go together", fn);
+  if (g.n_experts > MOE_MAX_EXPERTS) return fail(MOE_ERR_UNSUPPORTED, "%s: n_experts > %d", fn, MOE_MAX_EXPERTS);
+  if (g.k_dim % 128 != 0) return fail(MOE_ERR_UNSUPPORTED, "%s: k_dim must be a multiple of 128", fn);
+  // per-lane load offsets within a tile are 32-bit
+  if (g.k_dim > (int64_t(1) << 22) || g.n_dim > (int64_t(1) << 22))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: k_dim and n_dim must be at most %d", fn, 1 << 22);
+  if (g.n_rows > INT32_MAX) return fail(MOE_ERR_UNSUPPORTED, "%s: n_rows exceeds the int32 range", fn);
+  if (moe::gemm_mxfp4_tiles(g.n_rows, g.n_experts, g.n_dim) > INT32_MAX - 8)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: too many tiles", fn);
+  if (g.n_rows == 0) return MOE_OK;
+  if (!g.rows || !g.row_scales || !index || !g.w || !g.w_scales || !g.y)
+    return fail(MOE_ERR_ARG, "%s: null pointer argument", fn);
+  if (off(g.rows, 16) || off(g.w, 16) || off(g.w_up, 16) || off(g.y, 16))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: rows, weights and y must be 16-byte aligned", fn);
+  if (off(g.row_scales, 4) || off(g.w_scales, 4) || off(g.w_up_scales, 4) || off(index, 4))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: scales and indices must be 4-byte aligned", fn);
+  return MOE_OK;
+}
+}  // namespace
+
+int moe_quantize_mxfp4(const void* x, int32_t x_dtype, int64_t n_rows, int64_t k_dim,
+                       uint8_t* codes, uint8_t* scales, void* stream) {
+  const char* fn = "moe_quantize_mxfp4";
+  const int rc = check_mxfp4_rows(fn, x_dtype, n_rows, k_dim);
+  if (rc) return rc;
+  if (n_rows == 0) return ok();
+  if (!x || !codes || !scales) return fail(MOE_ERR_ARG, "%s: null pointer argument", fn);
+  if (off(x, 16) || off(codes, 4))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: x must be 16-byte and codes 4-byte aligned", fn);
+  return hip_status(moe::launch_quantize_mxfp4(x, x_dtype == MOE_BF16, n_rows * k_dim, codes, scales,
+                                               static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+int moe_dequant_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t n_rows, int64_t k_dim,
+                      void* out, int32_t out_dtype, void* stream) {
+  const char* fn = "moe_dequant_mxfp4";
+  const int rc = check_mxfp4_rows(fn, out_dtype, n_rows, k_dim);
+  if (rc) return rc;
+  if (n_rows == 0) return ok();
+  if (!codes || !scales || !out) return fail(MOE_ERR_ARG, "%s: null pointer argument", fn);
+  if (off(out, 16) || off(codes, 4))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: out must be 16-byte and codes 4-byte aligned", fn);
+  return hip_status(moe::launch_dequant_mxfp4(codes, scales, n_rows * k_dim, out,
+                                              out_dtype == MOE_BF16, static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+int moe_grouped_gemm_mxfp4(const uint8_t* rows, const uint8_t* row_scales, int64_t n_rows,
+                           int64_t k_dim, const int32_t* expert_offsets, int32_t n_experts,
+                           const uint8_t* w, const uint8_t* w_scales, const uint8_t* w_up,
+                           const uint8_t* w_up_scales, int64_t n_dim, void* y, void* stream) {
+  const char* fn = "moe_grouped_gemm_mxfp4";
+  const moe::Mxfp4Product g{rows, row_scales, n_rows, k_dim, n_experts, w, w_scales,
+                            w_up, w_up_scales, n_dim, y};
+  const int rc = check_mxfp4_product(fn, g, expert_offsets);
+  if (rc) return rc;
+  if (n_rows == 0) return ok();
+  return hip_status(moe::launch_grouped_gemm_mxfp4(g, expert_offsets, static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+size_t moe_gather_gemm_mxfp4_workspace_bytes(int64_t n_rows, int32_t n_experts) {
+  if (n_rows < 0 || n_rows > INT32_MAX || n_experts < 1 || n_experts > MOE_MAX_EXPERTS) return 0;
+  return moe::gather_gemm_mxfp4_workspace_bytes(n_rows, n_experts);
+}
+
+int moe_gather_gemm_mxfp4(const uint8_t* rows, const uint8_t* row_scales, int64_t n_rows,
+                          int64_t k_dim, const int32_t* row_expert, int32_t n_experts,
+                          const uint8_t* w, const uint8_t* w_scales, const uint8_t* w_up,
+                          const uint8_t* w_up_scales, int64_t n_dim, void* y, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_gather_gemm_mxfp4";
+  const moe::Mxfp4Product g{rows, row_scales, n_rows, k_dim, n_experts, w, w_scales,
+                            w_up, w_up_scales, n_dim, y};
+  const int rc = check_mxfp4_product(fn, g, row_expert);
+  if (rc) return rc;
+  if (n_rows == 0) return ok();
+  const size_t need = moe::gather_gemm_mxfp4_workspace_bytes(n_rows, n_experts);
+  if (!workspace || workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                workspace ? workspace_bytes : size_t(0));
+  if (off(workspace, 256))
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace must be 256-byte aligned", fn);
+  return hip_status(moe::launch_gather_gemm_mxfp4(g, row_expert, workspace, static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
 }  // extern "C"

@@ -144,4 +144,31 @@ hipError_t launch_grouped_gemm_fp8(const void* rows, const float* row_scales, in
                                    const void* w, const float* w_scales, int64_t n_dim, void* y,
                                    hipStream_t stream);
 
+// ---- MXFP4 (E2M1 codes two to a byte, one E8M0 scale per 32)
+hipError_t launch_quantize_mxfp4(const void* x, int x_bf16, int64_t n_elems, void* codes,
+                                 uint8_t* scales, hipStream_t stream);
+hipError_t launch_dequant_mxfp4(const void* codes, const uint8_t* scales, int64_t n_elems, void* out,
+                                int out_bf16, hipStream_t stream);
+
+// Operands of an expert product (K a multiple of 128); w_up null: no SwiGLU.
+struct Mxfp4Product {
+  const void* rows;
+  const uint8_t* row_scales;
+  int64_t n_rows, k_dim;
+  int n_experts;
+  const void* w;
+  const uint8_t* w_scales;
+  const void* w_up;
+  const uint8_t* w_up_scales;
+  int64_t n_dim;
+  void* y;
+};
+// Worst-case workgroup count, for the caller's int32 range check.
+int64_t gemm_mxfp4_tiles(int64_t n_rows, int n_experts, int64_t n_dim);
+hipError_t launch_grouped_gemm_mxfp4(const Mxfp4Product& g, const int32_t* expert_offsets,
+                                     hipStream_t stream);
+size_t gather_gemm_mxfp4_workspace_bytes(int64_t n_rows, int n_experts);
+hipError_t launch_gather_gemm_mxfp4(const Mxfp4Product& g, const int32_t* row_expert,
+                                    void* workspace, hipStream_t stream);
+
 }  // namespace moe

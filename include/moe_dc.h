@@ -483,6 +483,85 @@ int moe_grouped_gemm_fp8(const void* rows, const float* row_scales, int64_t n_ro
                          const void* w, const float* w_scales, int64_t n_dim, void* y,
                          void* stream);
 
+/* ---------------------------------------------------------------- MXFP4
+ * The OCP microscaling format MXFP4: E2M1 elements (bits s ee m; magnitudes 0,
+ * 0.5, 1, 1.5, 2, 3, 4, 6) and one E8M0 scale byte X, worth 2^(X - 127), per 32
+ * consecutive elements of a row; X = 255 is NaN.  Two codes share a byte, the
+ * even element in the low nibble: a row of K elements is K/2 code bytes and
+ * K/32 scale bytes.  Codes and scales are plain bytes, so moe_scatter_rows and
+ * moe_gather_rows dispatch them (a call for each): quantise a token once, then
+ * scatter it to its k rows.
+ *
+ * moe_quantize_mxfp4 -- with m the largest magnitude of a block and E its fp32
+ * exponent field (0 for subnormals and zero):
+ *   X    = max(E - 2, 0), i.e. 2^(X-127) = 2^(floor(log2 m) - 2) where E > 2
+ *   code = the E2M1 value nearest to x / 2^(X-127), ties to the even code,
+ *          magnitudes above 6 becoming 6, the sign kept (also of a zero)
+ * A block that holds a NaN or an infinity gets X = 255 and zero codes.
+ *   x [n_rows, K] of x_dtype (MOE_F32 or MOE_BF16), 16-byte aligned
+ *   codes [n_rows, K/2] uint8, output, 4-byte aligned
+ *   scales [n_rows, K/32] uint8, output
+ * Errors: MOE_ERR_ARG for null pointers (unless n_rows == 0), n_rows < 0,
+ * K < 1 or another dtype; MOE_ERR_UNSUPPORTED for K % 32 != 0, misaligned
+ * pointers or more than 2^40 elements. */
+int moe_quantize_mxfp4(const void* x, int32_t x_dtype, int64_t n_rows, int64_t k_dim,
+                       uint8_t* codes, uint8_t* scales, void* stream);
+
+/* moe_dequant_mxfp4 -- the values of MXFP4 rows (the identity expert of an
+ * MXFP4 payload): out[r, i] = value(code) * 2^(X - 127), rounded once to
+ * out_dtype (exact for what moe_quantize_mxfp4 wrote; 2^(X-127) up to 2^127
+ * can overflow to infinity); NaN where X = 255.
+ *   out [n_rows, K] of out_dtype (MOE_F32 or MOE_BF16), 16-byte aligned
+ * Errors: those of moe_quantize_mxfp4. */
+int moe_dequant_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t n_rows, int64_t k_dim,
+                      void* out, int32_t out_dtype, void* stream);
+
+/* moe_grouped_gemm_mxfp4 -- MXFP4 grouped expert product reading dispatched
+ * MXFP4 rows in place.  For expert e and every row p in
+ * [expert_offsets[e], expert_offsets[e+1]), with b over the K/32 blocks:
+ *   g[p, n] = sum_b 2^(row_scales[p,b] + w_scales[e,n,b] - 254)
+ *             * sum_{k in block b} value(rows[p,k]) * value(w[e,n,k])
+ *   y[p, n] = bf16( g[p, n] )                              w_up null
+ *   y[p, n] = bf16( silu(g[p, n]) * u[p, n] )              u: g with w_up
+ * Scaled 4-bit products on the matrix cores, fp32 accumulation in a fixed
+ * order, one rounding.  A scale byte of 255 in a row (in a column) makes the
+ * row's (the column's) outputs NaN.
+ *   rows            [n_rows, K/2] codes, 16-byte aligned
+ *   row_scales      [n_rows, K/32] uint8, 4-byte aligned
+ *   expert_offsets  [E+1] int32, device-resident, non-decreasing; rows outside
+ *                   [offsets[0], offsets[E]) are neither read nor written
+ *   w, w_up         [E, N, K/2] codes, 16-byte aligned; w_up may be null
+ *   w_scales, w_up_scales [E, N, K/32] uint8, 4-byte aligned
+ *   y               [n_rows, N] bfloat16, output, 16-byte aligned
+ * No workspace.  Errors: MOE_ERR_ARG for null pointers (unless n_rows == 0),
+ * n_rows < 0, sizes < 1 or w_up and w_up_scales not given together;
+ * MOE_ERR_UNSUPPORTED for K % 128 != 0, K or N above 2^22, E >
+ * MOE_MAX_EXPERTS, n_rows beyond the int32 range, too many tiles or misaligned
+ * pointers. */
+int moe_grouped_gemm_mxfp4(const uint8_t* rows, const uint8_t* row_scales, int64_t n_rows,
+                           int64_t k_dim, const int32_t* expert_offsets, int32_t n_experts,
+                           const uint8_t* w, const uint8_t* w_scales, const uint8_t* w_up,
+                           const uint8_t* w_up_scales, int64_t n_dim, void* y, void* stream);
+
+/* moe_gather_gemm_mxfp4_workspace_bytes -- workspace of moe_gather_gemm_mxfp4.
+ * 0 for invalid sizes. */
+size_t moe_gather_gemm_mxfp4_workspace_bytes(int64_t n_rows, int32_t n_experts);
+
+/* moe_gather_gemm_mxfp4 -- the product of moe_grouped_gemm_mxfp4 over rows left
+ * in any order, row r taking expert row_expert[r] (the unsorted dispatch;
+ * meant for few rows per expert, as moe_gather_swiglu).  y[r] lands at row r;
+ * rows whose id lies outside [0, E) leave y as it was.
+ *   row_expert  [n_rows] int32, device-resident
+ *   workspace   moe_gather_gemm_mxfp4_workspace_bytes(n_rows, E) bytes,
+ *               256-byte aligned, clobbered
+ * Errors: those of moe_grouped_gemm_mxfp4; MOE_ERR_WORKSPACE for a short or
+ * misaligned workspace. */
+int moe_gather_gemm_mxfp4(const uint8_t* rows, const uint8_t* row_scales, int64_t n_rows,
+                          int64_t k_dim, const int32_t* row_expert, int32_t n_experts,
+                          const uint8_t* w, const uint8_t* w_scales, const uint8_t* w_up,
+                          const uint8_t* w_up_scales, int64_t n_dim, void* y, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
