@@ -112,6 +112,338 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_kernel(
   }
 }
 
+// ---------------------------------------------------------------- many rows per expert
+// 256 x 256 tiles (SwiGLU: 128 columns of w and the same 128 of w_up), one
+// workgroup of 4 waves (2 x 2) per CU, a wave owning 128 x 128 as 4 x 4 MFMA
+// tiles whose 256 accumulators stay in registers: each operand byte read from
+// LDS feeds four MFMAs, half the LDS rate.
+//   * K advances in stages of 256, so a stage row is 128 bytes of codes, one
+//     line.  Direct global->LDS loads fill two 64 KB slots: stage d is
+//     multiplied from slot d % 2 while stage d + 1 lands in the other; the one
+//     barrier per stage publishes stage d + 1 and frees slot d % 2.
+//   * Lane half h multiplies 16-byte chunks 4h..4h+3 of its row, one per MFMA
+//     slice, so its four blocks of 32 have consecutive scale bytes: one dword
+//     per row and stage, the slice number picking the byte.
+//   * Scales skip LDS: 32 bytes of a row's scales cover four stages; lane half
+//     h loads 16 of them, and two swaps between the halves leave one register
+//     per stage in each lane.
+//   * Past K the scale bytes are 0 on both sides: whatever codes are there add
+//     36 * 2^-254, less than the smallest fp32.
+// LDS rows are XOR-swizzled in 16-byte chunks by (row >> 1) & 7: the rows that
+// a 16-lane phase of a ds_read_b128 reads fall in distinct bank groups.
+namespace big {
+
+constexpr int kBM = 256, kBN = 256;
+constexpr int kRowBytes = 128;                 // 256 codes
+constexpr int kTileBytes = kBM * kRowBytes;    // 32 KB per operand and stage
+constexpr int kSlotBytes = 2 * kTileBytes;
+constexpr int kLd = kTileBytes / (kThreads * 16);   // direct loads per lane, operand and stage (8)
+constexpr int kT = 4;                          // 32-row MFMA tiles of a wave, each way
+constexpr int kGroupM = 8;                     // row tiles per group of the tile order
+
+typedef __attribute__((address_space(3))) void* lds_ptr;
+typedef unsigned int u32x4a __attribute__((ext_vector_type(4), aligned(4)));
+
+// at most n vector-memory operations outstanding, LDS operations all returned
+constexpr unsigned wait_vm_lgkm0(int n) {
+  return unsigned(n & 15) | (unsigned((n >> 4) & 3) << 14) | (0x7u << 4);
+}
+constexpr unsigned wait_vm(int n) { return wait_vm_lgkm0(n) | (0xFu << 8); }
+
+// Sources of this lane's direct loads.  Run r = 4 i + wave of an operand tile
+// is its rows 8 r .. 8 r + 7; lane l fills row 8 r + l / 8, LDS chunk l % 8,
+// and so reads global chunk (l % 8) ^ ((row >> 1) & 7), the same for every i.
+struct Src {
+  const uint8_t* base[3];          // the tile's rows, w and w_up columns, at K = 0
+  uint32_t a_off[kLd], b_off[kLd]; // from those bases
+  uint32_t back;                   // taken off in the last stage where K ends inside it
+  int n_stages;
+};
+
+template <bool GLU, int LO, int HI>   // runs 0..7: rows, 8..15: columns
+__device__ __forceinline__ void load_runs(unsigned char* slot, const Src& s, int wave, int d) {
+  const bool last = d >= s.n_stages - 1;        // stages past the end repeat the last one
+  const int64_t k = int64_t(last ? s.n_stages - 1 : d) * kRowBytes;
+  const uint32_t back = last ? s.back : 0u;
+#pragma unroll
+  for (int i = LO; i < HI; ++i) {
+    const int run = ((i % kLd) * 4 + wave) * 1024;
+    const uint8_t* base = (i < kLd ? s.base[0] : s.base[GLU && i % kLd >= kLd / 2 ? 2 : 1]) + k;
+    const uint32_t o = (i < kLd ? s.a_off[i] : s.b_off[i - kLd]) - back;
+    __builtin_amdgcn_global_load_lds(base + o, (lds_ptr)(slot + (i < kLd ? 0 : kTileBytes) + run), 16, 0, 0);
+  }
+}
+
+struct Frag {
+  i32x4 a[kT], b[kT];
+};
+struct Lds {
+  int a_row, b_row[kT], chunk[4];
+};
+__device__ __forceinline__ void read_frag(const unsigned char* slot, const Lds& l, int kk, Frag& f) {
+#pragma unroll
+  for (int i = 0; i < kT; ++i)
+    f.a[i] = *reinterpret_cast<const i32x4*>(slot + l.a_row + i * 32 * kRowBytes + l.chunk[kk]);
+#pragma unroll
+  for (int j = 0; j < kT; ++j)
+    f.b[j] = *reinterpret_cast<const i32x4*>(slot + kTileBytes + l.b_row[j] + l.chunk[kk]);
+}
+
+template <int KK>
+__device__ __forceinline__ void mma(f32x16 (&acc)[kT][kT], const Frag& f, const int (&sa)[kT], const int (&sb)[kT]) {
+#pragma unroll
+  for (int i = 0; i < kT; ++i)
+#pragma unroll
+    for (int j = 0; j < kT; ++j) {
+      const i32x8 a = {f.a[i].x, f.a[i].y, f.a[i].z, f.a[i].w, 0, 0, 0, 0};
+      const i32x8 b = {f.b[j].x, f.b[j].y, f.b[j].z, f.b[j].w, 0, 0, 0, 0};
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc[i][j], 4, 4, KK, sa[i], KK, sb[j]);
+    }
+}
+
+// Issue order of one slice: 16 MFMAs, the first R each followed by an LDS
+// read, N direct loads spread between them.
+template <int R, int N>
+__device__ __forceinline__ void slice_order() {
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                     // MFMA
+    if (q < R) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);          // LDS read
+    if ((q * N) / 16 != ((q + 1) * N) / 16) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+  }
+}
+
+// Scale dwords of four stages for 8 rows (4 of each operand): [stage][row].
+struct Scales {
+  int a[4][kT], b[4][kT];
+};
+struct ScaleSrc {
+  const uint8_t* base[3];
+  uint32_t a_off[kT], b_off[kT];
+  int n_bytes;                     // K / 32
+};
+template <bool GLU>
+__device__ __forceinline__ void load_scales(const ScaleSrc& s, int super, int half, int (&raw)[2 * kT][4]) {
+  const uint32_t first = 32 * super + 16 * half;
+  if (32 * super + 32 <= s.n_bytes) {
+#pragma unroll
+    for (int i = 0; i < 2 * kT; ++i) {
+      const uint8_t* base = s.base[i < kT ? 0 : (GLU && i % kT >= 2 ? 2 : 1)];
+      const u32x4a q = *reinterpret_cast<const u32x4a*>(base + ((i < kT ? s.a_off[i % kT] : s.b_off[i % kT]) + first));
+      raw[i][0] = q.x; raw[i][1] = q.y; raw[i][2] = q.z; raw[i][3] = q.w;
+    }
+  } else {                                       // K ends in these four stages
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const bool in = int(first) + 4 * t < s.n_bytes;
+      const uint32_t o = in ? first + 4 * t : 0u;
+#pragma unroll
+      for (int i = 0; i < 2 * kT; ++i) {
+        const uint8_t* base = s.base[i < kT ? 0 : (GLU && i % kT >= 2 ? 2 : 1)];
+        const int v = *reinterpret_cast<const int*>(base + ((i < kT ? s.a_off[i % kT] : s.b_off[i % kT]) + o));
+        raw[i][t] = in ? v : 0;
+      }
+    }
+  }
+}
+// raw: lane half h holds dwords 4h..4h+3 of the 8; stage t wants dword 2t + h
+__device__ __forceinline__ void spread_scales(const int (&raw)[2 * kT][4], Scales& s) {
+#pragma unroll
+  for (int i = 0; i < 2 * kT; ++i) {
+    const auto x = __builtin_amdgcn_permlane32_swap(raw[i][0], raw[i][1], false, false);
+    const auto y = __builtin_amdgcn_permlane32_swap(raw[i][2], raw[i][3], false, false);
+    int(&d0)[kT] = i < kT ? s.a[0] : s.b[0];
+    int(&d1)[kT] = i < kT ? s.a[1] : s.b[1];
+    int(&d2)[kT] = i < kT ? s.a[2] : s.b[2];
+    int(&d3)[kT] = i < kT ? s.a[3] : s.b[3];
+    d0[i % kT] = x[0]; d2[i % kT] = x[1];
+    d1[i % kT] = y[0]; d3[i % kT] = y[1];
+  }
+}
+
+// Barrier that publishes the direct loads every wave has waited for.
+__device__ __forceinline__ void stage_barrier() {
+  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Stage d from `cur`; on entry f0 holds its slice 0 and the row half of stage
+// d + 1 is on its way into `nxt`; on exit f0 holds slice 0 of stage d + 1.
+template <bool GLU, int T>
+__device__ __forceinline__ void stage(f32x16 (&acc)[kT][kT], Frag& f0, Frag& f1, unsigned char* cur,
+                                      unsigned char* nxt, const Src& src, const Lds& l,
+                                      const Scales& sc, int wave, int d) {
+  __builtin_amdgcn_sched_barrier(0);
+  load_runs<GLU, kLd, 2 * kLd>(nxt, src, wave, d + 1);
+  read_frag(cur, l, 1, f1);
+  mma<0>(acc, f0, sc.a[T], sc.b[T]);
+  slice_order<2 * kT, kLd>();
+  __builtin_amdgcn_sched_barrier(0);
+  read_frag(cur, l, 2, f0);
+  mma<1>(acc, f1, sc.a[T], sc.b[T]);
+  slice_order<2 * kT, 0>();
+  __builtin_amdgcn_sched_barrier(0);
+  read_frag(cur, l, 3, f1);
+  mma<2>(acc, f0, sc.a[T], sc.b[T]);
+  slice_order<2 * kT, 0>();
+  __builtin_amdgcn_sched_barrier(0);
+  stage_barrier();                          // stage d + 1 landed everywhere; cur is free
+  __builtin_amdgcn_sched_barrier(0);
+  load_runs<GLU, 0, kLd>(cur, src, wave, d + 2);
+  read_frag(nxt, l, 0, f0);
+  mma<3>(acc, f1, sc.a[T], sc.b[T]);
+  slice_order<2 * kT, kLd>();
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Real row tiles of all experts, under find_tile's clamping.
+__device__ int count_tiles(const int32_t* __restrict__ offs, int n_experts, int n_rows) {
+  const int lane = lane_id();
+  int total = 0;
+  for (int c = 0; c < n_experts; c += kWave) {
+    const int e = c + lane;
+    int nt = 0;
+    if (e < n_experts) {
+      const int a = offs[e], b = offs[e + 1];
+      const int lo = a < 0 ? 0 : (a > n_rows ? n_rows : a);
+      const int hi = b < lo ? lo : (b > n_rows ? n_rows : b);
+      nt = (hi - lo) / kBM + ((hi - lo) % kBM != 0);
+    }
+    total += lane_value(wave_inclusive_scan(nt), kWave - 1);
+  }
+  return __builtin_amdgcn_readfirstlane(total);
+}
+
+// TAIL: the number of stages modulo 4, each its own straight line (exits in the
+// middle of the four-stage loop made the compiler move the accumulators).
+template <bool GLU, int TAIL>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void tile_kernel(const uint8_t* __restrict__ rows, const uint8_t* __restrict__ row_scales, int n_rows,
+                 int K, const int32_t* __restrict__ offs, int n_experts,
+                 const uint8_t* __restrict__ w, const uint8_t* __restrict__ w_scales,
+                 const uint8_t* __restrict__ w_up, const uint8_t* __restrict__ w_up_scales, int N,
+                 uint16_t* __restrict__ y, int n_tiles) {
+  // two arrays, so the compiler can tell the slot being loaded from the slot
+  // being read and adds no wait between them
+  __shared__ __align__(1024) unsigned char slot0[kSlotBytes];
+  __shared__ __align__(1024) unsigned char slot1[kSlotBytes];
+
+  // XCD x (workgroup b runs on XCD b % 8) takes a contiguous range of the
+  // grouped order: 8 row tiles x all column tiles, row tiles fastest
+  const int m_real = count_tiles(offs, n_experts, n_rows);
+  const int64_t tiles = int64_t(m_real) * n_tiles;
+  const int64_t per_xcd = (tiles + kXcds - 1) / kXcds;
+  const int64_t in_xcd = blockIdx.x / kXcds;
+  const int64_t tt = int64_t(blockIdx.x % kXcds) * per_xcd + in_xcd;
+  if (in_xcd >= per_xcd || tt >= tiles) return;
+  const int g = int(tt / (int64_t(kGroupM) * n_tiles));
+  const int gm = m_real - g * kGroupM < kGroupM ? m_real - g * kGroupM : kGroupM;
+  const int in_group = int(tt - int64_t(g) * kGroupM * n_tiles);
+  const Tile t = find_tile<kBM>(g * kGroupM + in_group % gm, offs, n_experts, n_rows);
+  if (!t.valid) return;
+  const int n_tile = in_group / gm;
+
+  constexpr int kCols = GLU ? kBN / 2 : kBN;     // output columns of a tile
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
+  const int wm = wave >> 1, wn = wave & 1, r32 = lane & 31, half = lane >> 5;
+  const int64_t col0 = int64_t(n_tile) * kCols;
+  const int64_t w_row0 = int64_t(t.expert) * N + col0;
+  const int cols = N - int(col0);                // columns left, at least 1
+  const int left = t.row_end - t.row0;           // rows left, at least 1
+
+  Src src;
+  src.n_stages = (K + 255) / 256;
+  src.base[0] = rows + int64_t(t.row0) * (K / 2);
+  src.base[1] = w + w_row0 * (K / 2);
+  src.base[2] = GLU ? w_up + w_row0 * (K / 2) : nullptr;
+  const int q8 = lane >> 3;
+  const int chunk = (lane & 7) ^ ((4 * wave + (q8 >> 1)) & 7);
+  src.back = K % 256 != 0 && chunk >= 4 ? 64u : 0u;
+#pragma unroll
+  for (int i = 0; i < kLd; ++i) {
+    const int row = (4 * i + wave) * 8 + q8;
+    const int ar = row < left ? row : left - 1;            // clamped rows are never stored
+    const int bc = GLU ? row & (kCols - 1) : row;
+    const int br = bc < cols ? bc : cols - 1;
+    src.a_off[i] = uint32_t(ar) * uint32_t(K / 2) + chunk * 16;
+    src.b_off[i] = uint32_t(br) * uint32_t(K / 2) + chunk * 16;
+  }
+  // B tile rows of fragment j: columns wn*128 + 32 j, or with SwiGLU columns
+  // wn*64 + 32 (j % 2) of w (j < 2) and of w_up
+  Lds l;
+  ScaleSrc ss;
+  ss.n_bytes = K / 32;
+  ss.base[0] = row_scales + int64_t(t.row0) * ss.n_bytes;
+  ss.base[1] = w_scales + w_row0 * ss.n_bytes;
+  ss.base[2] = GLU ? w_up_scales + w_row0 * ss.n_bytes : nullptr;
+  l.a_row = (wm * 128 + r32) * kRowBytes;
+#pragma unroll
+  for (int i = 0; i < kT; ++i) {
+    const int ar = wm * 128 + 32 * i + r32;
+    const int bc = (GLU ? wn * 64 + 32 * (i & 1) : wn * 128 + 32 * i) + r32;
+    l.b_row[i] = ((GLU && i >= 2 ? kCols : 0) + bc) * kRowBytes;
+    ss.a_off[i] = uint32_t(ar < left ? ar : left - 1) * uint32_t(ss.n_bytes);
+    ss.b_off[i] = uint32_t(bc < cols ? bc : cols - 1) * uint32_t(ss.n_bytes);
+  }
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) l.chunk[kk] = ((4 * half + kk) ^ ((r32 >> 1) & 7)) << 4;
+
+  f32x16 acc[kT][kT];
+#pragma unroll
+  for (int i = 0; i < kT; ++i)
+#pragma unroll
+    for (int j = 0; j < kT; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+
+  Frag f0, f1;
+  Scales sc;
+  int raw[2 * kT][4];
+  load_runs<GLU, 0, 2 * kLd>(slot0, src, wave, 0);
+  load_scales<GLU>(ss, 0, half, raw);
+  stage_barrier();                               // stage 0 landed
+  load_runs<GLU, 0, kLd>(slot1, src, wave, 1);
+  read_frag(slot0, l, 0, f0);
+  const int n_stages = src.n_stages;
+  int d = 0;
+  for (; d + 4 <= n_stages; d += 4) {
+    spread_scales(raw, sc);
+    if (TAIL || d + 4 < n_stages) load_scales<GLU>(ss, (d >> 2) + 1, half, raw);
+    stage<GLU, 0>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d);
+    stage<GLU, 1>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 1);
+    stage<GLU, 2>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d + 2);
+    stage<GLU, 3>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 3);
+  }
+  if constexpr (TAIL > 0) {
+    spread_scales(raw, sc);
+    stage<GLU, 0>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d);
+    if constexpr (TAIL > 1) stage<GLU, 1>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 1);
+    if constexpr (TAIL > 2) stage<GLU, 2>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d + 2);
+  }
+  __builtin_amdgcn_s_waitcnt(wait_vm(0));        // no direct load may outlive the workgroup
+
+  // lane holds C[8*(v/4) + 4*half + v%4][lane % 32] of each 32 x 32 tile
+#pragma unroll
+  for (int i = 0; i < kT; ++i)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int r = wm * 128 + 32 * i + 8 * (v >> 2) + 4 * half + (v & 3);
+      if (r >= left) continue;
+      uint16_t* out = y + int64_t(t.row0 + r) * N + col0;
+#pragma unroll
+      for (int j = 0; j < (GLU ? 2 : kT); ++j) {
+        const int c = (GLU ? wn * 64 : wn * 128) + 32 * j + r32;
+        const float o = GLU ? silu(acc[i][j][v]) * acc[i][j + (GLU ? 2 : 0)][v] : acc[i][j][v];
+        if (c < cols) out[c] = f32_to_bf16_rne(o);
+      }
+    }
+}
+
+}  // namespace big
+
 // Workspace of the gather form: the maps of a sorted dispatch of the ids.
 struct GatherLayout {
   size_t counts, offsets, seg_offsets, dst_pos, order, dispatch_ws, total;
@@ -138,6 +470,25 @@ hipError_t launch_product(const Mxfp4Product& g, const int32_t* offs, const int3
   const uint8_t *x = static_cast<const uint8_t*>(g.rows), *w = static_cast<const uint8_t*>(g.w),
                 *u = static_cast<const uint8_t*>(g.w_up);
   uint16_t* y = static_cast<uint16_t*>(g.y);
+  if (!order && g.n_rows >= 128 * g.n_experts) {
+    const int nt = int((g.n_dim + (u ? 127 : 255)) / (u ? 128 : 256));
+    const int64_t mt = (g.n_rows + big::kBM - 1) / big::kBM + g.n_experts;
+    const unsigned blocks = unsigned((mt * nt + kXcds - 1) / kXcds * kXcds);
+    auto run = [&](auto kernel) {
+      kernel<<<blocks, kThreads, 0, stream>>>(x, g.row_scales, int(g.n_rows), int(g.k_dim), offs, g.n_experts, w, g.w_scales, u, g.w_up_scales, int(g.n_dim), y, nt);
+    };
+    switch ((g.k_dim + 255) / 256 % 4 * 2 + (u ? 1 : 0)) {
+      case 0: run(big::tile_kernel<false, 0>); break;
+      case 1: run(big::tile_kernel<true, 0>); break;
+      case 2: run(big::tile_kernel<false, 1>); break;
+      case 3: run(big::tile_kernel<true, 1>); break;
+      case 4: run(big::tile_kernel<false, 2>); break;
+      case 5: run(big::tile_kernel<true, 2>); break;
+      case 6: run(big::tile_kernel<false, 3>); break;
+      default: run(big::tile_kernel<true, 3>); break;
+    }
+    return hipGetLastError();
+  }
   if (u)
     gemm_mxfp4_kernel<true><<<grid, kThreads, 0, stream>>>(x, g.row_scales, int(g.n_rows), int(g.k_dim), offs, g.n_experts, order, w, g.w_scales, u, g.w_up_scales, int(g.n_dim), y, n_tiles);
   else

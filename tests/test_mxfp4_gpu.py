@@ -261,6 +261,23 @@ def test_zero_rows():
     assert moe.moe_gather_gemm_mxfp4(z(0, 64), z(0, 4), i32(0), z(2, 8, 64), z(2, 8, 4)).shape == (0, 8)
 
 
+# at least 128 rows per expert: every number of 256-wide K stages modulo 4, with
+# and without a half stage at the end, row and column counts off the tile
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("k", [128, 256, 384, 512, 640, 896, 1024, 1280, 1408, 1792, 2176, 4224])
+def test_products_of_many_rows(k, glu):
+    rng = np.random.default_rng(k)
+    e, r, n = 3, 700, 300
+    rows, rs = _operand(rng, r, k)
+    w = _operand(rng, e, n, k)
+    up = _operand(rng, e, n, k) if glu else None
+    if glu:
+        rs, w = (rs - np.uint8(4)).astype(np.uint8), (w[0], (w[1] - np.uint8(3)).astype(np.uint8))
+    ids = np.sort(rng.choice(e, r, p=[0.5, 0.1, 0.4])).astype(np.int32)
+    with np.errstate(over="ignore"):
+        _check(to_np(_run("grouped", rows, rs, ids, w, up)), rows, rs, ids, w, up, f"K={k}")
+
+
 def test_weights_past_four_gibibytes():
     """Weight and output offsets beyond 2^32 bytes: the last expert of 4.6 GB."""
     e, n, k = 9, 65536, 16384
