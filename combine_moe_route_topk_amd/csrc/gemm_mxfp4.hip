@@ -17,9 +17,6 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kThreads = 256;
-constexpr int kTM = 32;           // rows per tile
-constexpr int kTN = 128;          // columns per workgroup: 32 per wave
 constexpr int kXcds = 8;
 
 struct Tile {
@@ -62,55 +59,219 @@ __device__ Tile find_tile(int m_idx, const int32_t* __restrict__ offs, int n_exp
   return t;
 }
 
-__device__ __forceinline__ i32x8 codes16(const uint8_t* p) {
-  const i32x4 q = *reinterpret_cast<const i32x4*>(p);
-  return i32x8{q.x, q.y, q.z, q.w, 0, 0, 0, 0};
-}
-
-__device__ __forceinline__ f32x16 mfma4(i32x8 a, i32x8 b, f32x16 c, int sa, int sb) {
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, 0, sa, 0, sb);
-}
-
 __device__ __forceinline__ float silu(float a) { return a / (1.f + expf(-a)); }
 
+// ---------------------------------------------------------------- few rows per expert
+// The weights are most of the bytes: each is read once per tile of 16 NB rows,
+// straight from memory into registers, 1024 elements of K of every weight row
+// in flight.  A workgroup of 8 waves takes one tile; a wave owns 32 weight rows
+// (SwiGLU: 16 of w and the same 16 of w_up, so silu(g) * u is lane-local) over
+// the whole K, as the A operand of v_mfma_scale_f32_16x16x128: lane (n, g) =
+// (l % 16, l / 16) holds row n and block 4 s + g of step s, so one load
+// instruction reads 64 consecutive bytes of 16 weight rows.  The tile's rows
+// are the B operand, staged through LDS 1024 elements at a time,
+// double-buffered, one barrier a stage, which leaves the memory queues to the
+// weights.  A lane ends with 4 consecutive columns of one row: 8-byte stores.
+namespace stream {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x4a __attribute__((ext_vector_type(4), aligned(4)));
+
+constexpr int kWaves = 8;
+constexpr int kStreamThreads = kWaves * kWave;
+constexpr int kWT = 2;                   // 16-row weight tiles per wave
+constexpr int kCh = 4;                   // K steps of 128 per chunk
+constexpr int kSt = 8;                   // K steps per LDS stage (1024 elements)
+constexpr int kPitch = kSt * 64 + 16;    // code bytes of a staged row: rows land 4 banks apart
+constexpr int kScPitch = kSt * 4 + 16;   // scale bytes of a staged row
+
+// Weight codes and scales of one chunk: tile t, step s.
+struct Chunk {
+  i32x4 q[kWT][kCh];
+  int sc[kWT][kCh];
+};
+
+__device__ __forceinline__ void load_chunk(Chunk& c, const uint8_t* const (&w)[kWT],
+                                           const uint8_t* const (&ws)[kWT], int step, int n_steps) {
+#pragma unroll
+  for (int t = 0; t < kWT; ++t) {
+    if (step + kCh <= n_steps) {
+      const u32x4a v = *reinterpret_cast<const u32x4a*>(ws[t] + 4 * step);
+#pragma unroll
+      for (int s = 0; s < kCh; ++s) {
+        c.q[t][s] = *reinterpret_cast<const i32x4*>(w[t] + 64 * (step + s));
+        c.sc[t][s] = v[s];
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < kCh; ++s)
+        if (step + s < n_steps) {
+          c.q[t][s] = *reinterpret_cast<const i32x4*>(w[t] + 64 * (step + s));
+          c.sc[t][s] = *reinterpret_cast<const int*>(ws[t] + 4 * (step + s));
+        }
+    }
+  }
+}
+
 // order: row p of the grouped order is row order[p] of rows and of y (null: p itself)
-template <bool GLU>
-__global__ __launch_bounds__(kThreads) void gemm_mxfp4_kernel(
+template <bool GLU, int NB>
+__global__ __launch_bounds__(kStreamThreads) void stream_kernel(
     const uint8_t* __restrict__ rows, const uint8_t* __restrict__ row_scales, int n_rows, int K,
     const int32_t* __restrict__ offs, int n_experts, const int32_t* __restrict__ order,
     const uint8_t* __restrict__ w, const uint8_t* __restrict__ w_scales,
     const uint8_t* __restrict__ w_up, const uint8_t* __restrict__ w_up_scales, int N,
-    uint16_t* __restrict__ y, int n_tiles) {
+    uint16_t* __restrict__ y, int n_groups) {
+  constexpr int kTM = 16 * NB;
+  constexpr int kPieces = kTM * kSt * 4 / kStreamThreads;      // 16-byte staging loads per thread (NB)
+  static_assert(kPieces * kStreamThreads == kTM * kSt * 4, "whole staging loads");
+  static_assert(kTM * kSt <= kStreamThreads, "one scale dword per thread");
+  __shared__ __align__(16) unsigned char s_q[2][kTM * kPitch];
+  __shared__ __align__(16) unsigned char s_sc[2][kTM * kScPitch];
+
+  // workgroup b runs on XCD b % 8; XCD x takes row tiles x, x + 8, ..., all
+  // column groups of one back to back (its rows stay in that XCD's L2); the
+  // unused tail of the worst-case grid is spread evenly
   const int b = blockIdx.x;
   const int slot = b / kXcds;
-  const int m_idx = (slot / n_tiles) * kXcds + b % kXcds, n_tile = slot % n_tiles;
-  const Tile t = find_tile<kTM>(m_idx, offs, n_experts, n_rows);
-  if (!t.valid) return;
-  const int lane = lane_id(), r = lane & 31, half = lane >> 5;
-  const int64_t col0 = int64_t(n_tile) * kTN + __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave) * 32;
-  int p = t.row0 + r < t.row_end ? t.row0 + r : t.row_end - 1;    // clamped rows are never stored
-  if (order) p = order[p];
-  const int64_t n = col0 + r < N ? col0 + r : N - 1;
-  const int64_t wr = int64_t(t.expert) * N + n;
-  const int kb = K / 32;
-  f32x16 acc = {}, up = {};
-  for (int i = half; i < kb; i += 2) {                            // K is a multiple of 64
-    const i32x8 a = codes16(rows + int64_t(p) * (K / 2) + i * 16);
-    const int sa = row_scales[int64_t(p) * kb + i];
-    acc = mfma4(a, codes16(w + wr * (K / 2) + i * 16), acc, sa, w_scales[wr * kb + i]);
-    if (GLU) up = mfma4(a, codes16(w_up + wr * (K / 2) + i * 16), up, sa, w_up_scales[wr * kb + i]);
-  }
-  // lane holds C[8*(v/4) + 4*half + v%4][lane % 32]
-  if (col0 + r >= N) return;
+  const int m_idx = (slot / n_groups) * kXcds + b % kXcds, grp = slot % n_groups;
+  const Tile tile = find_tile<kTM>(m_idx, offs, n_experts, n_rows);
+  if (!tile.valid) return;                                     // whole workgroup
+
+  const int tid = threadIdx.x, lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int n = lane & 15, g = lane >> 4;
+  constexpr int kCols = GLU ? 16 : 16 * kWT;                   // output columns per wave
+  const int col0 = (grp * kWaves + wave) * kCols;
+  const bool active = col0 < N;         // a wave past the last column still stages rows
+  const int n_steps = K / 128, kb = K / 32;
+
+  // staging: piece tid + threads * j is row p / 32 and 16-byte column p % 32 of
+  // the stage; rows past the end of the tile repeat its first (never stored)
+  const uint8_t* a_src[kPieces];
+  int a_lds[kPieces], a_col[kPieces];
 #pragma unroll
-  for (int v = 0; v < 16; ++v) {
-    int g = t.row0 + 8 * (v >> 2) + 4 * half + (v & 3);
-    if (g >= t.row_end) continue;
-    if (order) g = order[g];
-    const float o = GLU ? silu(acc[v]) * up[v] : acc[v];
-    y[int64_t(g) * N + col0 + r] = f32_to_bf16_rne(o);
+  for (int j = 0; j < kPieces; ++j) {
+    const int p = tid + kStreamThreads * j;
+    const int row = p / (kSt * 4);
+    a_col[j] = p % (kSt * 4);
+    int r = tile.row0 + (tile.row0 + row < tile.row_end ? row : 0);
+    if (order) r = order[r];
+    a_src[j] = rows + int64_t(r) * (K / 2) + a_col[j] * 16;
+    a_lds[j] = row * kPitch + a_col[j] * 16;
+  }
+  const int sc_row = tid / kSt, sc_step = tid % kSt;           // threads below kTM * kSt
+  const bool sc_has = sc_row < kTM;
+  int sr = tile.row0 + (sc_has && tile.row0 + sc_row < tile.row_end ? sc_row : 0);
+  if (order) sr = order[sr];
+  const uint8_t* sc_src = row_scales + int64_t(sr) * kb + 4 * sc_step;
+
+  const uint8_t *w_ptr[kWT], *ws_ptr[kWT];
+#pragma unroll
+  for (int t = 0; t < kWT; ++t) {
+    int c = GLU ? col0 + n : col0 + 16 * t + n;
+    if (c >= N) c = N - 1;                                     // partial last group; never stored
+    const int64_t wr = int64_t(tile.expert) * N + c;
+    w_ptr[t] = (GLU && t ? w_up : w) + wr * (K / 2) + 16 * g;
+    ws_ptr[t] = (GLU && t ? w_up_scales : w_scales) + wr * kb;
+  }
+
+  f32x4 acc[kWT][NB];
+#pragma unroll
+  for (int t = 0; t < kWT; ++t)
+#pragma unroll
+    for (int i = 0; i < NB; ++i) acc[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  Chunk ring[2];
+  if (active) {
+    load_chunk(ring[0], w_ptr, ws_ptr, 0, n_steps);
+    if (kCh < n_steps) load_chunk(ring[1], w_ptr, ws_ptr, kCh, n_steps);
+  }
+  i32x4 stg[kPieces];
+  int stg_sc = 0;
+  auto fetch = [&](int step) {                                 // the stage that begins at `step`
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j)
+      if (step + a_col[j] / 4 < n_steps) stg[j] = *reinterpret_cast<const i32x4*>(a_src[j] + 64 * step);
+    if (sc_has && step + sc_step < n_steps) stg_sc = *reinterpret_cast<const int*>(sc_src + 4 * step);
+  };
+  auto put = [&](int buf) {
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) *reinterpret_cast<i32x4*>(&s_q[buf][a_lds[j]]) = stg[j];
+    if (sc_has) *reinterpret_cast<int*>(&s_sc[buf][sc_row * kScPitch + 4 * sc_step]) = stg_sc;
+  };
+#pragma unroll
+  for (int j = 0; j < kPieces; ++j) stg[j] = i32x4{0, 0, 0, 0};
+  fetch(0);
+  put(0);
+  __syncthreads();
+
+  for (int st = 0; st < n_steps; st += kSt) {
+    const int buf = (st / kSt) & 1;
+    const bool more = st + kSt < n_steps;
+    if (more) fetch(st + kSt);
+    if (active) {
+      const unsigned char* q = s_q[buf] + n * kPitch + 16 * g;
+      const unsigned char* sc = s_sc[buf] + n * kScPitch + g;
+#pragma unroll
+      for (int c = 0; c < kSt / kCh; ++c) {
+        const int step0 = st + c * kCh;
+        if (step0 < n_steps) {
+#pragma unroll
+          for (int s = 0; s < kCh; ++s) {
+            if (step0 + s < n_steps) {
+              i32x8 bq[NB];
+              int bs[NB];
+#pragma unroll
+              for (int i = 0; i < NB; ++i) {
+                const i32x4 v = *reinterpret_cast<const i32x4*>(q + i * 16 * kPitch + 64 * (c * kCh + s));
+                bq[i] = i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+                bs[i] = sc[i * 16 * kScPitch + 4 * (c * kCh + s)];
+              }
+#pragma unroll
+              for (int t = 0; t < kWT; ++t) {
+                const i32x4 v = ring[c].q[t][s];
+                const i32x8 a = {v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+                const int as = int(uint32_t(ring[c].sc[t][s]) >> (8 * g));
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+                  acc[t][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, bq[i], acc[t][i], 4, 4, 0, as, 0, bs[i]);
+              }
+            }
+          }
+          if (step0 + 2 * kCh < n_steps) load_chunk(ring[c], w_ptr, ws_ptr, step0 + 2 * kCh, n_steps);
+        }
+      }
+    }
+    // the other buffer was last read in the stage before, which every wave has left
+    if (more) put(buf ^ 1);
+    __syncthreads();
+  }
+  if (!active) return;
+
+  // lane holds columns 4 g .. 4 g + 3 of row n of each 16 x 16 tile
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const int p = tile.row0 + 16 * i + n;
+    if (p >= tile.row_end) continue;
+    uint16_t* out = y + int64_t(order ? order[p] : p) * N;
+#pragma unroll
+    for (int t = 0; t < (GLU ? 1 : kWT); ++t) {
+      const int c = col0 + 16 * t + 4 * g;
+      float o[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) o[v] = GLU ? silu(acc[0][i][v]) * acc[1][i][v] : acc[t][i][v];
+      if (N % 4 == 0) {                                        // whole groups of 4, 8-byte aligned
+        if (c < N) *reinterpret_cast<uint2*>(out + c) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+      } else {
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (c + v < N) out[c + v] = f32_to_bf16_rne(o[v]);
+      }
+    }
   }
 }
+
+}  // namespace stream
 
 // ---------------------------------------------------------------- many rows per expert
 // 256 x 256 tiles (SwiGLU: 128 columns of w and the same 128 of w_up), one
@@ -133,6 +294,7 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_kernel(
 // a 16-lane phase of a ds_read_b128 reads fall in distinct bank groups.
 namespace big {
 
+constexpr int kThreads = 256;
 constexpr int kBM = 256, kBN = 256;
 constexpr int kRowBytes = 128;                 // 256 codes
 constexpr int kTileBytes = kBM * kRowBytes;    // 32 KB per operand and stage
@@ -464,9 +626,6 @@ GatherLayout gather_layout(int64_t n_rows, int n_experts) {
 
 hipError_t launch_product(const Mxfp4Product& g, const int32_t* offs, const int32_t* order,
                           hipStream_t stream) {
-  const int n_tiles = int((g.n_dim + kTN - 1) / kTN);
-  const int64_t m = (g.n_rows + kTM - 1) / kTM + g.n_experts;
-  const unsigned grid = unsigned((m + kXcds - 1) / kXcds * kXcds * n_tiles);
   const uint8_t *x = static_cast<const uint8_t*>(g.rows), *w = static_cast<const uint8_t*>(g.w),
                 *u = static_cast<const uint8_t*>(g.w_up);
   uint16_t* y = static_cast<uint16_t*>(g.y);
@@ -475,7 +634,7 @@ hipError_t launch_product(const Mxfp4Product& g, const int32_t* offs, const int3
     const int64_t mt = (g.n_rows + big::kBM - 1) / big::kBM + g.n_experts;
     const unsigned blocks = unsigned((mt * nt + kXcds - 1) / kXcds * kXcds);
     auto run = [&](auto kernel) {
-      kernel<<<blocks, kThreads, 0, stream>>>(x, g.row_scales, int(g.n_rows), int(g.k_dim), offs, g.n_experts, w, g.w_scales, u, g.w_up_scales, int(g.n_dim), y, nt);
+      kernel<<<blocks, big::kThreads, 0, stream>>>(x, g.row_scales, int(g.n_rows), int(g.k_dim), offs, g.n_experts, w, g.w_scales, u, g.w_up_scales, int(g.n_dim), y, nt);
     };
     switch ((g.k_dim + 255) / 256 % 4 * 2 + (u ? 1 : 0)) {
       case 0: run(big::tile_kernel<false, 0>); break;
@@ -489,17 +648,28 @@ hipError_t launch_product(const Mxfp4Product& g, const int32_t* offs, const int3
     }
     return hipGetLastError();
   }
-  if (u)
-    gemm_mxfp4_kernel<true><<<grid, kThreads, 0, stream>>>(x, g.row_scales, int(g.n_rows), int(g.k_dim), offs, g.n_experts, order, w, g.w_scales, u, g.w_up_scales, int(g.n_dim), y, n_tiles);
-  else
-    gemm_mxfp4_kernel<false><<<grid, kThreads, 0, stream>>>(x, g.row_scales, int(g.n_rows), int(g.k_dim), offs, g.n_experts, order, w, g.w_scales, u, g.w_up_scales, int(g.n_dim), y, n_tiles);
+  const int cols = stream::kWaves * (u ? 16 : 32);
+  const int groups = int((g.n_dim + cols - 1) / cols);
+  auto run = [&](auto kernel, int tm) {
+    const int64_t m = (g.n_rows + tm - 1) / tm + g.n_experts;
+    const unsigned grid = unsigned((m + kXcds - 1) / kXcds * kXcds * groups);
+    kernel<<<grid, stream::kStreamThreads, 0, stream>>>(x, g.row_scales, int(g.n_rows), int(g.k_dim), offs, g.n_experts, order, w, g.w_scales, u, g.w_up_scales, int(g.n_dim), y, groups);
+  };
+  const int64_t mean = g.n_rows / g.n_experts;
+  if (mean < 12) {
+    if (u) run(stream::stream_kernel<true, 1>, 16);
+    else run(stream::stream_kernel<false, 1>, 16);
+  } else {
+    if (u) run(stream::stream_kernel<true, 4>, 64);
+    else run(stream::stream_kernel<false, 4>, 64);
+  }
   return hipGetLastError();
 }
 
 }  // namespace
 
 int64_t gemm_mxfp4_tiles(int64_t n_rows, int n_experts, int64_t n_dim) {
-  return ((n_rows + kTM - 1) / kTM + n_experts + kXcds) * ((n_dim + kTN - 1) / kTN);
+  return ((n_rows + 15) / 16 + n_experts + kXcds) * ((n_dim + 127) / 128);
 }
 
 size_t gather_gemm_mxfp4_workspace_bytes(int64_t n_rows, int n_experts) {
