@@ -6,6 +6,8 @@
 // The matrix cores take the format as it is: v_mfma_scale_f32_32x32x64_f8f6f4
 // reads 32 codes (16 bytes) and their scale byte per lane and operand, lane l
 // holding row l % 32 and the block of 32 that l / 32 names.
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "launch.hpp"
 
@@ -77,54 +79,29 @@ namespace stream {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x4a __attribute__((ext_vector_type(4), aligned(4)));
 
-constexpr int kWaves = 8;
-constexpr int kStreamThreads = kWaves * kWave;
 constexpr int kWT = 2;                   // 16-row weight tiles per wave
 constexpr int kCh = 4;                   // K steps of 128 per chunk
-constexpr int kSt = 8;                   // K steps per LDS stage (1024 elements)
+constexpr int kSt = 8;                   // K steps per LDS stage (1024 elements), all in flight
 constexpr int kPitch = kSt * 64 + 16;    // code bytes of a staged row: rows land 4 banks apart
 constexpr int kScPitch = kSt * 4 + 16;   // scale bytes of a staged row
 
-// Weight codes and scales of one chunk: tile t, step s.
-struct Chunk {
-  i32x4 q[kWT][kCh];
-  int sc[kWT][kCh];
-};
-
-__device__ __forceinline__ void load_chunk(Chunk& c, const uint8_t* const (&w)[kWT],
-                                           const uint8_t* const (&ws)[kWT], int step, int n_steps) {
-#pragma unroll
-  for (int t = 0; t < kWT; ++t) {
-    if (step + kCh <= n_steps) {
-      const u32x4a v = *reinterpret_cast<const u32x4a*>(ws[t] + 4 * step);
-#pragma unroll
-      for (int s = 0; s < kCh; ++s) {
-        c.q[t][s] = *reinterpret_cast<const i32x4*>(w[t] + 64 * (step + s));
-        c.sc[t][s] = v[s];
-      }
-    } else {
-#pragma unroll
-      for (int s = 0; s < kCh; ++s)
-        if (step + s < n_steps) {
-          c.q[t][s] = *reinterpret_cast<const i32x4*>(w[t] + 64 * (step + s));
-          c.sc[t][s] = *reinterpret_cast<const int*>(ws[t] + 4 * (step + s));
-        }
-    }
-  }
-}
-
 // order: row p of the grouped order is row order[p] of rows and of y (null: p itself)
-template <bool GLU, int NB>
-__global__ __launch_bounds__(kStreamThreads) void stream_kernel(
+// X4: K is a multiple of 512, so a row's scales are read four steps at a time.
+// The loop over K has no other branches: past K the last step is read again
+// and multiplied by zero codes (loads under a branch made the compiler move
+// the products away from them and keep copies of what they multiply).
+template <bool GLU, int NB, int WAVES, bool X4>
+__global__ __launch_bounds__(WAVES * kWave) void stream_kernel(
     const uint8_t* __restrict__ rows, const uint8_t* __restrict__ row_scales, int n_rows, int K,
     const int32_t* __restrict__ offs, int n_experts, const int32_t* __restrict__ order,
     const uint8_t* __restrict__ w, const uint8_t* __restrict__ w_scales,
     const uint8_t* __restrict__ w_up, const uint8_t* __restrict__ w_up_scales, int N,
     uint16_t* __restrict__ y, int n_groups) {
   constexpr int kTM = 16 * NB;
-  constexpr int kPieces = kTM * kSt * 4 / kStreamThreads;      // 16-byte staging loads per thread (NB)
-  static_assert(kPieces * kStreamThreads == kTM * kSt * 4, "whole staging loads");
-  static_assert(kTM * kSt <= kStreamThreads, "one scale dword per thread");
+  constexpr int kThreads = WAVES * kWave;
+  constexpr int kPieces = kTM * kSt * 4 / kThreads;            // 16-byte staging loads per thread
+  constexpr int kScPieces = (kTM * kSt + kThreads - 1) / kThreads;   // and scale dwords
+  static_assert(kPieces * kThreads == kTM * kSt * 4, "whole staging loads");
   __shared__ __align__(16) unsigned char s_q[2][kTM * kPitch];
   __shared__ __align__(16) unsigned char s_sc[2][kTM * kScPitch];
 
@@ -141,29 +118,34 @@ __global__ __launch_bounds__(kStreamThreads) void stream_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int n = lane & 15, g = lane >> 4;
   constexpr int kCols = GLU ? 16 : 16 * kWT;                   // output columns per wave
-  const int col0 = (grp * kWaves + wave) * kCols;
-  const bool active = col0 < N;         // a wave past the last column still stages rows
+  const int col0 = (grp * WAVES + wave) * kCols;
   const int n_steps = K / 128, kb = K / 32;
 
   // staging: piece tid + threads * j is row p / 32 and 16-byte column p % 32 of
   // the stage; rows past the end of the tile repeat its first (never stored)
   const uint8_t* a_src[kPieces];
-  int a_lds[kPieces], a_col[kPieces];
+  int a_lds[kPieces];
+  const int a_step = tid % (kSt * 4) / 4;
 #pragma unroll
   for (int j = 0; j < kPieces; ++j) {
-    const int p = tid + kStreamThreads * j;
+    const int p = tid + kThreads * j;
     const int row = p / (kSt * 4);
-    a_col[j] = p % (kSt * 4);
     int r = tile.row0 + (tile.row0 + row < tile.row_end ? row : 0);
     if (order) r = order[r];
-    a_src[j] = rows + int64_t(r) * (K / 2) + a_col[j] * 16;
-    a_lds[j] = row * kPitch + a_col[j] * 16;
+    a_src[j] = rows + int64_t(r) * (K / 2) + 16 * (tid % 4);
+    a_lds[j] = row * kPitch + (p % (kSt * 4)) * 16;
   }
-  const int sc_row = tid / kSt, sc_step = tid % kSt;           // threads below kTM * kSt
-  const bool sc_has = sc_row < kTM;
-  int sr = tile.row0 + (sc_has && tile.row0 + sc_row < tile.row_end ? sc_row : 0);
-  if (order) sr = order[sr];
-  const uint8_t* sc_src = row_scales + int64_t(sr) * kb + 4 * sc_step;
+  const uint8_t* sc_src[kScPieces];
+  int sc_lds[kScPieces];
+  const int sc_step = tid % kSt;
+#pragma unroll
+  for (int j = 0; j < kScPieces; ++j) {
+    const int row = (tid + kThreads * j) / kSt % kTM;          // the spare threads repeat rows
+    int r = tile.row0 + (tile.row0 + row < tile.row_end ? row : 0);
+    if (order) r = order[r];
+    sc_src[j] = row_scales + int64_t(r) * kb;
+    sc_lds[j] = row * kScPitch + 4 * sc_step;
+  }
 
   const uint8_t *w_ptr[kWT], *ws_ptr[kWT];
 #pragma unroll
@@ -181,72 +163,102 @@ __global__ __launch_bounds__(kStreamThreads) void stream_kernel(
 #pragma unroll
     for (int i = 0; i < NB; ++i) acc[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  Chunk ring[2];
-  if (active) {
-    load_chunk(ring[0], w_ptr, ws_ptr, 0, n_steps);
-    if (kCh < n_steps) load_chunk(ring[1], w_ptr, ws_ptr, kCh, n_steps);
-  }
+  // step k of a stage lives in q[.][k], refilled for the next stage four steps
+  // at a time: whole lines of a weight row are asked for together (refilled
+  // step by step, as soon as each is multiplied, was 13-22% slower)
+  i32x4 q[kWT][kSt];
+  int sc[kWT][kSt];
+  auto clamp = [&](int step) { return step < n_steps ? step : n_steps - 1; };
+  auto refill = [&](int k, int step) {     // q[.][k .. k + 3] from `step`
+#pragma unroll
+    for (int t = 0; t < kWT; ++t) {
+      if (X4) {
+        const u32x4a v = *reinterpret_cast<const u32x4a*>(ws_ptr[t] + 4 * (clamp(step) / kCh * kCh));
+#pragma unroll
+        for (int i = 0; i < kCh; ++i) sc[t][k + i] = v[i];
+      }
+#pragma unroll
+      for (int i = 0; i < kCh; ++i) {
+        q[t][k + i] = *reinterpret_cast<const i32x4*>(w_ptr[t] + 64 * clamp(step + i));
+        if (!X4) sc[t][k + i] = *reinterpret_cast<const int*>(ws_ptr[t] + 4 * clamp(step + i));
+      }
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kSt; k += kCh) refill(k, k);
+
   i32x4 stg[kPieces];
-  int stg_sc = 0;
+  int stg_sc[kScPieces];
   auto fetch = [&](int step) {                                 // the stage that begins at `step`
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j)
-      if (step + a_col[j] / 4 < n_steps) stg[j] = *reinterpret_cast<const i32x4*>(a_src[j] + 64 * step);
-    if (sc_has && step + sc_step < n_steps) stg_sc = *reinterpret_cast<const int*>(sc_src + 4 * step);
+    for (int j = 0; j < kPieces; ++j) {
+      const int s = a_step + step;
+      stg[j] = *reinterpret_cast<const i32x4*>(a_src[j] + 64 * clamp(s));
+      stg[j] = s < n_steps ? stg[j] : i32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int j = 0; j < kScPieces; ++j)
+      stg_sc[j] = *reinterpret_cast<const int*>(sc_src[j] + 4 * clamp(sc_step + step));
   };
   auto put = [&](int buf) {
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) *reinterpret_cast<i32x4*>(&s_q[buf][a_lds[j]]) = stg[j];
-    if (sc_has) *reinterpret_cast<int*>(&s_sc[buf][sc_row * kScPitch + 4 * sc_step]) = stg_sc;
-  };
 #pragma unroll
-  for (int j = 0; j < kPieces; ++j) stg[j] = i32x4{0, 0, 0, 0};
+    for (int j = 0; j < kScPieces; ++j) *reinterpret_cast<int*>(&s_sc[buf][sc_lds[j]]) = stg_sc[j];
+  };
   fetch(0);
   put(0);
   __syncthreads();
 
-  for (int st = 0; st < n_steps; st += kSt) {
+  // the stage that begins at step st; MORE: there is another one
+  auto stage = [&](int st, auto more) {
+    constexpr bool MORE = decltype(more)::value;
     const int buf = (st / kSt) & 1;
-    const bool more = st + kSt < n_steps;
-    if (more) fetch(st + kSt);
-    if (active) {
-      const unsigned char* q = s_q[buf] + n * kPitch + 16 * g;
-      const unsigned char* sc = s_sc[buf] + n * kScPitch + g;
+    if constexpr (MORE) fetch(st + kSt);
+    const unsigned char* bq_base = s_q[buf] + n * kPitch + 16 * g;
+    const unsigned char* bs_base = s_sc[buf] + n * kScPitch + g;
 #pragma unroll
-      for (int c = 0; c < kSt / kCh; ++c) {
-        const int step0 = st + c * kCh;
-        if (step0 < n_steps) {
+    for (int k = 0; k < kSt; ++k) {
+      i32x8 bq[NB];
+      int bs[NB];
 #pragma unroll
-          for (int s = 0; s < kCh; ++s) {
-            if (step0 + s < n_steps) {
-              i32x8 bq[NB];
-              int bs[NB];
+      for (int i = 0; i < NB; ++i) {
+        const i32x4 v = *reinterpret_cast<const i32x4*>(bq_base + i * 16 * kPitch + 64 * k);
+        bq[i] = i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+        bs[i] = bs_base[i * 16 * kScPitch + 4 * k];
+      }
 #pragma unroll
-              for (int i = 0; i < NB; ++i) {
-                const i32x4 v = *reinterpret_cast<const i32x4*>(q + i * 16 * kPitch + 64 * (c * kCh + s));
-                bq[i] = i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
-                bs[i] = sc[i * 16 * kScPitch + 4 * (c * kCh + s)];
-              }
+      for (int t = 0; t < kWT; ++t) {
+        i32x4 v = q[t][k];
+        asm volatile("" : "+v"(v));        // keeps the loop's copies four registers wide
+        const i32x8 a = {v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+        const int as = int(uint32_t(sc[t][k]) >> (8 * g));
 #pragma unroll
-              for (int t = 0; t < kWT; ++t) {
-                const i32x4 v = ring[c].q[t][s];
-                const i32x8 a = {v.x, v.y, v.z, v.w, 0, 0, 0, 0};
-                const int as = int(uint32_t(ring[c].sc[t][s]) >> (8 * g));
-#pragma unroll
-                for (int i = 0; i < NB; ++i)
-                  acc[t][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, bq[i], acc[t][i], 4, 4, 0, as, 0, bs[i]);
-              }
-            }
-          }
-          if (step0 + 2 * kCh < n_steps) load_chunk(ring[c], w_ptr, ws_ptr, step0 + 2 * kCh, n_steps);
-        }
+        for (int i = 0; i < NB; ++i)
+          acc[t][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, bq[i], acc[t][i], 4, 4, 0, as, 0, bs[i]);
+      }
+      if (MORE && k % kCh == kCh - 1) {
+        __builtin_amdgcn_sched_barrier(0); // the refills stay where they are
+        refill(k + 1 - kCh, st + kSt + k + 1 - kCh);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
-    // the other buffer was last read in the stage before, which every wave has left
-    if (more) put(buf ^ 1);
-    __syncthreads();
-  }
-  if (!active) return;
+    if constexpr (MORE) {
+      // the other buffer was last read in the stage before, which every wave has left
+      put(buf ^ 1);
+      __syncthreads();
+    }
+  };
+  int st = 0;
+  for (; st + kSt < n_steps; st += kSt) stage(st, std::true_type());
+  stage(st, std::false_type());
+  // the products end here, with every lane on: moved into the divergent stores
+  // below, the shifts of their scales would skip the lanes that store nothing
+#pragma unroll
+  for (int t = 0; t < kWT; ++t)
+#pragma unroll
+    for (int i = 0; i < NB; ++i) asm volatile("" : "+v"(acc[t][i]));
+  if (col0 >= N) return;
 
   // lane holds columns 4 g .. 4 g + 3 of row n of each 16 x 16 tile
 #pragma unroll
@@ -586,6 +598,11 @@ void tile_kernel(const uint8_t* __restrict__ rows, const uint8_t* __restrict__ r
     if constexpr (TAIL > 2) stage<GLU, 2>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d + 2);
   }
   __builtin_amdgcn_s_waitcnt(wait_vm(0));        // no direct load may outlive the workgroup
+  // the products end here, with every lane on, not in the divergent stores below
+#pragma unroll
+  for (int i = 0; i < kT; ++i)
+#pragma unroll
+    for (int j = 0; j < kT; ++j) asm volatile("" : "+a"(acc[i][j]));
 
   // lane holds C[8*(v/4) + 4*half + v%4][lane % 32] of each 32 x 32 tile
 #pragma unroll
@@ -624,6 +641,12 @@ GatherLayout gather_layout(int64_t n_rows, int n_experts) {
   return L;
 }
 
+// Row tiles at most: every expert can end in a partial one, and each holds a row.
+int64_t most_tiles(int64_t n_rows, int n_experts, int tm) {
+  const int64_t m = (n_rows + tm - 1) / tm + n_experts;
+  return m < n_rows ? m : n_rows;
+}
+
 hipError_t launch_product(const Mxfp4Product& g, const int32_t* offs, const int32_t* order,
                           hipStream_t stream) {
   const uint8_t *x = static_cast<const uint8_t*>(g.rows), *w = static_cast<const uint8_t*>(g.w),
@@ -631,7 +654,7 @@ hipError_t launch_product(const Mxfp4Product& g, const int32_t* offs, const int3
   uint16_t* y = static_cast<uint16_t*>(g.y);
   if (!order && g.n_rows >= 128 * g.n_experts) {
     const int nt = int((g.n_dim + (u ? 127 : 255)) / (u ? 128 : 256));
-    const int64_t mt = (g.n_rows + big::kBM - 1) / big::kBM + g.n_experts;
+    const int64_t mt = most_tiles(g.n_rows, g.n_experts, big::kBM);
     const unsigned blocks = unsigned((mt * nt + kXcds - 1) / kXcds * kXcds);
     auto run = [&](auto kernel) {
       kernel<<<blocks, big::kThreads, 0, stream>>>(x, g.row_scales, int(g.n_rows), int(g.k_dim), offs, g.n_experts, w, g.w_scales, u, g.w_up_scales, int(g.n_dim), y, nt);
@@ -648,21 +671,27 @@ hipError_t launch_product(const Mxfp4Product& g, const int32_t* offs, const int3
     }
     return hipGetLastError();
   }
-  const int cols = stream::kWaves * (u ? 16 : 32);
-  const int groups = int((g.n_dim + cols - 1) / cols);
-  auto run = [&](auto kernel, int tm) {
-    const int64_t m = (g.n_rows + tm - 1) / tm + g.n_experts;
+  auto run = [&](auto kernel, int tm, int waves) {
+    const int cols = waves * (u ? 16 : 32);
+    const int groups = int((g.n_dim + cols - 1) / cols);
+    const int64_t m = most_tiles(g.n_rows, g.n_experts, tm);
     const unsigned grid = unsigned((m + kXcds - 1) / kXcds * kXcds * groups);
-    kernel<<<grid, stream::kStreamThreads, 0, stream>>>(x, g.row_scales, int(g.n_rows), int(g.k_dim), offs, g.n_experts, order, w, g.w_scales, u, g.w_up_scales, int(g.n_dim), y, groups);
+    kernel<<<grid, waves * kWave, 0, stream>>>(x, g.row_scales, int(g.n_rows), int(g.k_dim), offs, g.n_experts, order, w, g.w_scales, u, g.w_up_scales, int(g.n_dim), y, groups);
   };
   const int64_t mean = g.n_rows / g.n_experts;
-  if (mean < 12) {
-    if (u) run(stream::stream_kernel<true, 1>, 16);
-    else run(stream::stream_kernel<false, 1>, 16);
-  } else {
-    if (u) run(stream::stream_kernel<true, 4>, 64);
-    else run(stream::stream_kernel<false, 4>, 64);
-  }
+  constexpr int W = 4;
+  auto pick = [&](auto glu, auto nb) {
+    constexpr bool G = decltype(glu)::value;
+    constexpr int NB = decltype(nb)::value;
+    if (g.k_dim % 512 == 0) run(stream::stream_kernel<G, NB, W, true>, 16 * NB, W);
+    else run(stream::stream_kernel<G, NB, W, false>, 16 * NB, W);
+  };
+  auto by_rows = [&](auto glu) {
+    if (mean < 12) pick(glu, std::integral_constant<int, 1>());
+    else pick(glu, std::integral_constant<int, 4>());
+  };
+  if (u) by_rows(std::true_type());
+  else by_rows(std::false_type());
   return hipGetLastError();
 }
 
