@@ -61,7 +61,32 @@ __device__ Tile find_tile(int m_idx, const int32_t* __restrict__ offs, int n_exp
   return t;
 }
 
-__device__ __forceinline__ float silu(float a) { return a / (1.f + expf(-a)); }
+// silu(a) = a / (1 + e^-a) from the exponential and reciprocal instructions (1
+// ulp each): about 2^-21 off, beside the 2^-8 of the bf16 rounding that follows.
+// a = -inf gives NaN as a / (1 + e^-a) does.
+__device__ __forceinline__ float silu(float a) {
+  return a * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(a * -1.44269504f));
+}
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {   // rounds to nearest even
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
+// Columns c .. c + 3 of a row of n (c a multiple of 4): 8 bytes where rows are
+// multiples of 8 bytes, else element by element.
+__device__ __forceinline__ void store4(uint16_t* row, int c, int n, bool whole, const float (&o)[4]) {
+  const uint32_t lo = pack2(o[0], o[1]), hi = pack2(o[2], o[3]);
+  if (whole) {
+    if (c < n) *reinterpret_cast<uint2*>(row + c) = make_uint2(lo, hi);
+  } else {
+    if (c < n) row[c] = uint16_t(lo);
+    if (c + 1 < n) row[c + 1] = uint16_t(lo >> 16);
+    if (c + 2 < n) row[c + 2] = uint16_t(hi);
+    if (c + 3 < n) row[c + 3] = uint16_t(hi >> 16);
+  }
+}
 
 // ---------------------------------------------------------------- few rows per expert
 // The weights are most of the bytes: each is read once per tile of 16 NB rows,
@@ -272,13 +297,7 @@ __global__ __launch_bounds__(WAVES * kWave) void stream_kernel(
       float o[4];
 #pragma unroll
       for (int v = 0; v < 4; ++v) o[v] = GLU ? silu(acc[0][i][v]) * acc[1][i][v] : acc[t][i][v];
-      if (N % 4 == 0) {                                        // whole groups of 4, 8-byte aligned
-        if (c < N) *reinterpret_cast<uint2*>(out + c) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
-      } else {
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          if (c + v < N) out[c + v] = f32_to_bf16_rne(o[v]);
-      }
+      store4(out, c, N, N % 4 == 0, o);
     }
   }
 }
@@ -371,7 +390,7 @@ __device__ __forceinline__ void mma(f32x16 (&acc)[kT][kT], const Frag& f, const 
     for (int j = 0; j < kT; ++j) {
       const i32x8 a = {f.a[i].x, f.a[i].y, f.a[i].z, f.a[i].w, 0, 0, 0, 0};
       const i32x8 b = {f.b[j].x, f.b[j].y, f.b[j].z, f.b[j].w, 0, 0, 0, 0};
-      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc[i][j], 4, 4, KK, sa[i], KK, sb[j]);
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc[i][j], 4, 4, KK, sb[j], KK, sa[i]);
     }
 }
 
@@ -604,21 +623,24 @@ void tile_kernel(const uint8_t* __restrict__ rows, const uint8_t* __restrict__ r
 #pragma unroll
     for (int j = 0; j < kT; ++j) asm volatile("" : "+a"(acc[i][j]));
 
-  // lane holds C[8*(v/4) + 4*half + v%4][lane % 32] of each 32 x 32 tile
+  // lane holds columns 8*(v/4) + 4*half + v%4 of row lane % 32 of each 32 x 32 tile
 #pragma unroll
-  for (int i = 0; i < kT; ++i)
+  for (int i = 0; i < kT; ++i) {
+    const int r = wm * 128 + 32 * i + r32;
+    if (r >= left) continue;
+    uint16_t* out = y + int64_t(t.row0 + r) * N + col0;
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int r = wm * 128 + 32 * i + 8 * (v >> 2) + 4 * half + (v & 3);
-      if (r >= left) continue;
-      uint16_t* out = y + int64_t(t.row0 + r) * N + col0;
+    for (int j = 0; j < (GLU ? 2 : kT); ++j)
 #pragma unroll
-      for (int j = 0; j < (GLU ? 2 : kT); ++j) {
-        const int c = (GLU ? wn * 64 : wn * 128) + 32 * j + r32;
-        const float o = GLU ? silu(acc[i][j][v]) * acc[i][j + (GLU ? 2 : 0)][v] : acc[i][j][v];
-        if (c < cols) out[c] = f32_to_bf16_rne(o);
+      for (int v = 0; v < 16; v += 4) {
+        const int c = (GLU ? wn * 64 : wn * 128) + 32 * j + 2 * v + 4 * half;
+        float o[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          o[u] = GLU ? silu(acc[i][j][v + u]) * acc[i][j + (GLU ? 2 : 0)][v + u] : acc[i][j][v + u];
+        store4(out, c, cols, N % 4 == 0, o);
       }
-    }
+  }
 }
 
 }  // namespace big
