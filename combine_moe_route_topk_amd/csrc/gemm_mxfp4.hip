@@ -463,16 +463,17 @@ __device__ __forceinline__ void stage_barrier() {
 }
 
 // Stage d from `cur`; on entry f0 holds its slice 0 and the row half of stage
-// d + 1 is on its way into `nxt`; on exit f0 holds slice 0 of stage d + 1.
-template <bool GLU, int T>
+// d + 1, if there is one, is on its way into `nxt`.  LEFT: stages after this
+// one (2 for more than that); unless it is the last, f0 ends as slice 0 of the next.
+template <bool GLU, int T, int LEFT>
 __device__ __forceinline__ void stage(f32x16 (&acc)[kT][kT], Frag& f0, Frag& f1, unsigned char* cur,
                                       unsigned char* nxt, const Src& src, const Lds& l,
                                       const Scales& sc, int wave, int d) {
   __builtin_amdgcn_sched_barrier(0);
-  load_runs<GLU, kLd, 2 * kLd>(nxt, src, wave, d + 1);
+  if (LEFT > 0) load_runs<GLU, kLd, 2 * kLd>(nxt, src, wave, d + 1);
   read_frag(cur, l, 1, f1);
   mma<0>(acc, f0, sc.a[T], sc.b[T]);
-  slice_order<2 * kT, kLd>();
+  slice_order<2 * kT, (LEFT > 0 ? kLd : 0)>();
   __builtin_amdgcn_sched_barrier(0);
   read_frag(cur, l, 2, f0);
   mma<1>(acc, f1, sc.a[T], sc.b[T]);
@@ -482,12 +483,14 @@ __device__ __forceinline__ void stage(f32x16 (&acc)[kT][kT], Frag& f0, Frag& f1,
   mma<2>(acc, f0, sc.a[T], sc.b[T]);
   slice_order<2 * kT, 0>();
   __builtin_amdgcn_sched_barrier(0);
-  stage_barrier();                          // stage d + 1 landed everywhere; cur is free
-  __builtin_amdgcn_sched_barrier(0);
-  load_runs<GLU, 0, kLd>(cur, src, wave, d + 2);
-  read_frag(nxt, l, 0, f0);
+  if (LEFT > 0) {
+    stage_barrier();                        // stage d + 1 landed everywhere; cur is free
+    __builtin_amdgcn_sched_barrier(0);
+    if (LEFT > 1) load_runs<GLU, 0, kLd>(cur, src, wave, d + 2);
+    read_frag(nxt, l, 0, f0);
+  }
   mma<3>(acc, f1, sc.a[T], sc.b[T]);
-  slice_order<2 * kT, kLd>();
+  slice_order<(LEFT > 0 ? 2 * kT : 0), (LEFT > 1 ? kLd : 0)>();
   __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -509,8 +512,9 @@ __device__ int count_tiles(const int32_t* __restrict__ offs, int n_experts, int 
   return __builtin_amdgcn_readfirstlane(total);
 }
 
-// TAIL: the number of stages modulo 4, each its own straight line (exits in the
-// middle of the four-stage loop made the compiler move the accumulators).
+// TAIL: the stages of the last group of up to four, each count its own straight
+// line (exits in the middle of the four-stage loop made the compiler move the
+// accumulators).
 template <bool GLU, int TAIL>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void tile_kernel(const uint8_t* __restrict__ rows, const uint8_t* __restrict__ row_scales, int n_rows,
@@ -598,24 +602,23 @@ void tile_kernel(const uint8_t* __restrict__ rows, const uint8_t* __restrict__ r
   load_runs<GLU, 0, 2 * kLd>(slot0, src, wave, 0);
   load_scales<GLU>(ss, 0, half, raw);
   stage_barrier();                               // stage 0 landed
-  load_runs<GLU, 0, kLd>(slot1, src, wave, 1);
-  read_frag(slot0, l, 0, f0);
   const int n_stages = src.n_stages;
+  if (n_stages > 1) load_runs<GLU, 0, kLd>(slot1, src, wave, 1);
+  read_frag(slot0, l, 0, f0);
   int d = 0;
-  for (; d + 4 <= n_stages; d += 4) {
+  for (; d + TAIL < n_stages; d += 4) {
     spread_scales(raw, sc);
-    if (TAIL || d + 4 < n_stages) load_scales<GLU>(ss, (d >> 2) + 1, half, raw);
-    stage<GLU, 0>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d);
-    stage<GLU, 1>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 1);
-    stage<GLU, 2>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d + 2);
-    stage<GLU, 3>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 3);
+    load_scales<GLU>(ss, (d >> 2) + 1, half, raw);
+    stage<GLU, 0, 2>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d);
+    stage<GLU, 1, 2>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 1);
+    stage<GLU, 2, 2>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d + 2);
+    stage<GLU, 3, 2>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 3);
   }
-  if constexpr (TAIL > 0) {
-    spread_scales(raw, sc);
-    stage<GLU, 0>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d);
-    if constexpr (TAIL > 1) stage<GLU, 1>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 1);
-    if constexpr (TAIL > 2) stage<GLU, 2>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d + 2);
-  }
+  spread_scales(raw, sc);
+  stage<GLU, 0, TAIL - 1>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d);
+  if constexpr (TAIL > 1) stage<GLU, 1, TAIL - 2>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 1);
+  if constexpr (TAIL > 2) stage<GLU, 2, TAIL - 3>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d + 2);
+  if constexpr (TAIL > 3) stage<GLU, 3, 0>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 3);
   __builtin_amdgcn_s_waitcnt(wait_vm(0));        // no direct load may outlive the workgroup
   // the products end here, with every lane on, not in the divergent stores below
 #pragma unroll
@@ -681,15 +684,15 @@ hipError_t launch_product(const Mxfp4Product& g, const int32_t* offs, const int3
     auto run = [&](auto kernel) {
       kernel<<<blocks, big::kThreads, 0, stream>>>(x, g.row_scales, int(g.n_rows), int(g.k_dim), offs, g.n_experts, w, g.w_scales, u, g.w_up_scales, int(g.n_dim), y, nt);
     };
-    switch ((g.k_dim + 255) / 256 % 4 * 2 + (u ? 1 : 0)) {
-      case 0: run(big::tile_kernel<false, 0>); break;
-      case 1: run(big::tile_kernel<true, 0>); break;
-      case 2: run(big::tile_kernel<false, 1>); break;
-      case 3: run(big::tile_kernel<true, 1>); break;
-      case 4: run(big::tile_kernel<false, 2>); break;
-      case 5: run(big::tile_kernel<true, 2>); break;
-      case 6: run(big::tile_kernel<false, 3>); break;
-      default: run(big::tile_kernel<true, 3>); break;
+    switch (((g.k_dim + 255) / 256 - 1) % 4 * 2 + (u ? 1 : 0)) {
+      case 0: run(big::tile_kernel<false, 1>); break;
+      case 1: run(big::tile_kernel<true, 1>); break;
+      case 2: run(big::tile_kernel<false, 2>); break;
+      case 3: run(big::tile_kernel<true, 2>); break;
+      case 4: run(big::tile_kernel<false, 3>); break;
+      case 5: run(big::tile_kernel<true, 3>); break;
+      case 6: run(big::tile_kernel<false, 4>); break;
+      default: run(big::tile_kernel<true, 4>); break;
     }
     return hipGetLastError();
   }
