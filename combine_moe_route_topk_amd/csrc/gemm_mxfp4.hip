@@ -110,12 +110,45 @@ constexpr int kSt = 8;                   // K steps per LDS stage (1024 elements
 constexpr int kPitch = kSt * 64 + 16;    // code bytes of a staged row: rows land 4 banks apart
 constexpr int kScPitch = kSt * 4 + 16;   // scale bytes of a staged row
 
-// order: row p of the grouped order is row order[p] of rows and of y (null: p itself)
+// Up to 64 rows in any order: tile m of 16 rows of one expert, found in every
+// wave without a grouping pass before the product.  Lane q holds row q's
+// expert; the lanes with the same one come from a ballot per bit of the ids, a
+// tile begins at every 16th of them, and tiles are numbered by where they
+// begin.  Row i of the tile goes to s_rows[i], the tile's row_end is their
+// number.  Every lane calls it.
+__device__ __forceinline__ Tile direct_tile(int m, const int32_t* __restrict__ row_expert, int n_rows,
+                                            int n_experts, int* s_rows) {
+  const int lane = lane_id();
+  const int mine = lane < n_rows ? row_expert[lane] : -1;
+  const bool ok = unsigned(mine) < unsigned(n_experts);        // ids below 2^10
+  uint64_t same = ballot(ok);
+#pragma unroll
+  for (int bit = 1; bit < kMaxExperts; bit <<= 1) {
+    const uint64_t on = ballot(mine & bit);
+    same &= mine & bit ? on : ~on;
+  }
+  const int rank = __popcll(same & lanemask_lt());
+  const uint64_t begins = ballot(ok && rank % 16 == 0);
+  Tile t{};
+  const uint64_t at = ballot(((begins >> lane) & 1) && __popcll(begins & lanemask_lt()) == m);
+  if (!at) return t;                                           // fewer tiles
+  const int q = __ffsll((unsigned long long)at) - 1;
+  t.expert = lane_value(mine, q);
+  const int i = rank - lane_value(rank, q);
+  const bool in = ok && mine == t.expert && unsigned(i) < 16u;
+  if (in) s_rows[i] = lane;
+  t.row_end = __popcll(ballot(in));
+  t.valid = true;
+  return t;
+}
+
+// order: row p of the grouped order is row order[p] of rows and of y (null: p
+// itself).  DIRECT (up to 64 rows, NB 1): offs holds the expert of each row.
 // X4: K is a multiple of 512, so a row's scales are read four steps at a time.
 // The loop over K has no other branches: past K the last step is read again
 // and multiplied by zero codes (loads under a branch made the compiler move
 // the products away from them and keep copies of what they multiply).
-template <bool GLU, int NB, int WAVES, bool X4>
+template <bool GLU, int NB, int WAVES, bool X4, bool DIRECT>
 __global__ __launch_bounds__(WAVES * kWave) void stream_kernel(
     const uint8_t* __restrict__ rows, const uint8_t* __restrict__ row_scales, int n_rows, int K,
     const int32_t* __restrict__ offs, int n_experts, const int32_t* __restrict__ order,
@@ -132,14 +165,29 @@ __global__ __launch_bounds__(WAVES * kWave) void stream_kernel(
 
   // workgroup b runs on XCD b % 8; XCD x takes row tiles x, x + 8, ..., all
   // column groups of one back to back (its rows stay in that XCD's L2); the
-  // unused tail of the worst-case grid is spread evenly
+  // unused tail of the worst-case grid is spread evenly.  (Row tiles of one
+  // expert on one XCD, side by side, measured 0-16% slower: the last-level cache
+  // already serves their second reading of its weights.)
   const int b = blockIdx.x;
   const int slot = b / kXcds;
   const int m_idx = (slot / n_groups) * kXcds + b % kXcds, grp = slot % n_groups;
-  const Tile tile = find_tile<kTM>(m_idx, offs, n_experts, n_rows);
-  if (!tile.valid) return;                                     // whole workgroup
-
   const int tid = threadIdx.x, lane = lane_id();
+  __shared__ int s_rows[DIRECT ? kTM : 1];
+  Tile tile{};
+  if constexpr (DIRECT) {
+    static_assert(kTM == 16 && kMaxExperts <= 1024, "tiles of 16 rows, ids of 10 bits");
+    tile = direct_tile(m_idx, offs, n_rows, n_experts, s_rows);
+  } else {
+    tile = find_tile<kTM>(m_idx, offs, n_experts, n_rows);
+  }
+  if (!tile.valid) return;                                     // whole workgroup
+  if (DIRECT) __syncthreads();
+  // row i of the tile in rows and y; past the last one its first
+  auto row_at = [&](int i) {
+    const int p = tile.row0 + (tile.row0 + i < tile.row_end ? i : 0);
+    return DIRECT ? s_rows[p] : (order ? order[p] : p);
+  };
+
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int n = lane & 15, g = lane >> 4;
   constexpr int kCols = GLU ? 16 : 16 * kWT;                   // output columns per wave
@@ -155,9 +203,7 @@ __global__ __launch_bounds__(WAVES * kWave) void stream_kernel(
   for (int j = 0; j < kPieces; ++j) {
     const int p = tid + kThreads * j;
     const int row = p / (kSt * 4);
-    int r = tile.row0 + (tile.row0 + row < tile.row_end ? row : 0);
-    if (order) r = order[r];
-    a_src[j] = rows + int64_t(r) * (K / 2) + 16 * (tid % 4);
+    a_src[j] = rows + int64_t(row_at(row)) * (K / 2) + 16 * (tid % 4);
     a_lds[j] = row * kPitch + (p % (kSt * 4)) * 16;
   }
   const uint8_t* sc_src[kScPieces];
@@ -166,9 +212,7 @@ __global__ __launch_bounds__(WAVES * kWave) void stream_kernel(
 #pragma unroll
   for (int j = 0; j < kScPieces; ++j) {
     const int row = (tid + kThreads * j) / kSt % kTM;          // the spare threads repeat rows
-    int r = tile.row0 + (tile.row0 + row < tile.row_end ? row : 0);
-    if (order) r = order[r];
-    sc_src[j] = row_scales + int64_t(r) * kb;
+    sc_src[j] = row_scales + int64_t(row_at(row)) * kb;
     sc_lds[j] = row * kScPitch + 4 * sc_step;
   }
 
@@ -288,9 +332,8 @@ __global__ __launch_bounds__(WAVES * kWave) void stream_kernel(
   // lane holds columns 4 g .. 4 g + 3 of row n of each 16 x 16 tile
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
-    const int p = tile.row0 + 16 * i + n;
-    if (p >= tile.row_end) continue;
-    uint16_t* out = y + int64_t(order ? order[p] : p) * N;
+    if (tile.row0 + 16 * i + n >= tile.row_end) continue;
+    uint16_t* out = y + int64_t(row_at(16 * i + n)) * N;
 #pragma unroll
     for (int t = 0; t < (GLU ? 1 : kWT); ++t) {
       const int c = col0 + 16 * t + 4 * g;
@@ -666,6 +709,14 @@ GatherLayout gather_layout(int64_t n_rows, int n_experts) {
   return L;
 }
 
+// Mean rows per expert from which tiles of 32 rows are taken, of 64 rows, and
+// the 256 x 256 kernel.  Measured (rows per expert: times in us of 16-, 32-,
+// 64-row tiles and the 256 x 256 kernel; 64 experts, K = N = 4096): 8: 104,
+// 108, 114, 144; 16: 138, 120, 116, 143; 32: 212, 148, 121, 149; 48: 288, 186,
+// 138, 160; 64: 366, 225, 163, 162; 128: 678, 393, 255, 179.  With 8 experts
+// 32-row tiles lead up to 24: 14.7 against 23.4 and 16.1.
+constexpr int kNarrowRows = 10, kMiddleRows = 24, kManyRows = 64;
+
 // Row tiles at most: every expert can end in a partial one, and each holds a row.
 int64_t most_tiles(int64_t n_rows, int n_experts, int tm) {
   const int64_t m = (n_rows + tm - 1) / tm + n_experts;
@@ -677,7 +728,7 @@ hipError_t launch_product(const Mxfp4Product& g, const int32_t* offs, const int3
   const uint8_t *x = static_cast<const uint8_t*>(g.rows), *w = static_cast<const uint8_t*>(g.w),
                 *u = static_cast<const uint8_t*>(g.w_up);
   uint16_t* y = static_cast<uint16_t*>(g.y);
-  if (!order && g.n_rows >= 128 * g.n_experts) {
+  if (!order && g.n_rows >= int64_t(kManyRows) * g.n_experts) {
     const int nt = int((g.n_dim + (u ? 127 : 255)) / (u ? 128 : 256));
     const int64_t mt = most_tiles(g.n_rows, g.n_experts, big::kBM);
     const unsigned blocks = unsigned((mt * nt + kXcds - 1) / kXcds * kXcds);
@@ -708,15 +759,43 @@ hipError_t launch_product(const Mxfp4Product& g, const int32_t* offs, const int3
   auto pick = [&](auto glu, auto nb) {
     constexpr bool G = decltype(glu)::value;
     constexpr int NB = decltype(nb)::value;
-    if (g.k_dim % 512 == 0) run(stream::stream_kernel<G, NB, W, true>, 16 * NB, W);
-    else run(stream::stream_kernel<G, NB, W, false>, 16 * NB, W);
+    if (g.k_dim % 512 == 0) run(stream::stream_kernel<G, NB, W, true, false>, 16 * NB, W);
+    else run(stream::stream_kernel<G, NB, W, false, false>, 16 * NB, W);
   };
   auto by_rows = [&](auto glu) {
-    if (mean < 12) pick(glu, std::integral_constant<int, 1>());
+    if (mean < kNarrowRows) pick(glu, std::integral_constant<int, 1>());
+    else if (mean < kMiddleRows) pick(glu, std::integral_constant<int, 2>());
     else pick(glu, std::integral_constant<int, 4>());
   };
   if (u) by_rows(std::true_type());
   else by_rows(std::false_type());
+  return hipGetLastError();
+}
+
+// Rows up to which the gather form groups them inside the product's launch.
+constexpr int kDirectRows = 64;
+
+hipError_t launch_direct(const Mxfp4Product& g, const int32_t* row_expert, hipStream_t stream) {
+  constexpr int W = 4;
+  const int cols = W * (g.w_up ? 16 : 32);
+  const int groups = int((g.n_dim + cols - 1) / cols);
+  const int64_t m = most_tiles(g.n_rows, g.n_experts, 16);
+  const unsigned grid = unsigned((m + kXcds - 1) / kXcds * kXcds * groups);
+  auto run = [&](auto kernel) {
+    kernel<<<grid, W * kWave, 0, stream>>>(
+        static_cast<const uint8_t*>(g.rows), g.row_scales, int(g.n_rows), int(g.k_dim), row_expert,
+        g.n_experts, nullptr, static_cast<const uint8_t*>(g.w), g.w_scales,
+        static_cast<const uint8_t*>(g.w_up), g.w_up_scales, int(g.n_dim),
+        static_cast<uint16_t*>(g.y), groups);
+  };
+  const bool x4 = g.k_dim % 512 == 0;
+  if (g.w_up) {
+    if (x4) run(stream::stream_kernel<true, 1, W, true, true>);
+    else run(stream::stream_kernel<true, 1, W, false, true>);
+  } else {
+    if (x4) run(stream::stream_kernel<false, 1, W, true, true>);
+    else run(stream::stream_kernel<false, 1, W, false, true>);
+  }
   return hipGetLastError();
 }
 
@@ -737,6 +816,8 @@ hipError_t launch_grouped_gemm_mxfp4(const Mxfp4Product& g, const int32_t* exper
 
 hipError_t launch_gather_gemm_mxfp4(const Mxfp4Product& g, const int32_t* row_expert,
                                     void* workspace, hipStream_t stream) {
+  if (g.n_rows <= kDirectRows && g.n_rows < int64_t(kNarrowRows) * g.n_experts)
+    return launch_direct(g, row_expert, stream);
   const GatherLayout L = gather_layout(g.n_rows, g.n_experts);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   DispatchArgs d{};
