@@ -42,17 +42,20 @@ def _launch(fn: str, dev: torch.device, stream, args, own=()) -> None:
     device and stream are current.  `own`: tensors allocated in the call; on
     another stream than the current one their memory must not be handed out
     again before that stream has passed the call."""
-    cur = torch.cuda.current_stream(dev)
+    # the raw handle: torch.cuda.current_stream() takes 2 us to build its object
+    cur = torch._C._cuda_getCurrentRawStream(dev.index)
     if stream is None:
-        stream = cur
+        raw = cur
     elif stream.device != dev:
         raise ValueError(f"{fn}: the stream is on {stream.device}, the operands on {dev}")
+    else:
+        raw = stream.cuda_stream
     if dev.index == torch.cuda.current_device():
-        check(fn, getattr(lib, fn)(*args, _stream(stream)))
+        check(fn, getattr(lib, fn)(*args, raw))
     else:
         with torch.cuda.device(dev):
-            check(fn, getattr(lib, fn)(*args, _stream(stream)))
-    if stream != cur:
+            check(fn, getattr(lib, fn)(*args, raw))
+    if raw != cur:
         for t in own:
             t.record_stream(stream)
 
@@ -399,13 +402,15 @@ def moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, dst_pos: torch.Te
     if d_y is None:
         d_y = torch.empty_like(y)
         own.append(d_y)
+    else:
+        _need(d_y, "d_y", (y.dtype,), dev)
+        _shape(d_y, "d_y", y.shape)
     if d_topk_w is None:
         d_topk_w = torch.empty_like(topk_w)
         own.append(d_topk_w)
-    _need(d_y, "d_y", (y.dtype,), dev)
-    _shape(d_y, "d_y", y.shape)
-    _need(d_topk_w, "d_topk_w", (torch.float32,), dev)
-    _shape(d_topk_w, "d_topk_w", (n, k))
+    else:
+        _need(d_topk_w, "d_topk_w", (torch.float32,), dev)
+        _shape(d_topk_w, "d_topk_w", (n, k))
     _launch("moe_combine_backward", dev, stream,
             (_ptr(d_out), _FLOAT_IO[d_out.dtype], _ptr(y), _FLOAT_IO[y.dtype], n, hidden, k,
              _ptr(dst_pos), _ptr(topk_w), _ptr(d_y), _ptr(d_topk_w)), own)
@@ -425,10 +430,13 @@ def moe_dispatch_backward(d_rows: torch.Tensor, dst_pos: torch.Tensor, k: int,
     n, hidden = d_rows.shape[0] // k, d_rows.shape[1]
     own = []
     if d_x is None:
-        d_x = torch.empty((n, hidden), dtype=out_dtype or d_rows.dtype, device=dev)
+        d_x = d_rows.new_empty((n, hidden), dtype=out_dtype or d_rows.dtype)
         own.append(d_x)
-    _need(d_x, "d_x", tuple(_FLOAT_IO), dev)
-    _shape(d_x, "d_x", (n, hidden))
+        if d_x.dtype not in _FLOAT_IO:
+            raise TypeError(f"out_dtype is {out_dtype}, expected one of {tuple(_FLOAT_IO)}")
+    else:
+        _need(d_x, "d_x", tuple(_FLOAT_IO), dev)
+        _shape(d_x, "d_x", (n, hidden))
     _launch("moe_dispatch_backward", dev, stream,
             (_ptr(d_rows), _FLOAT_IO[d_rows.dtype], n, hidden, k, _ptr(dst_pos), _ptr(d_x),
              _FLOAT_IO[d_x.dtype]), own)
@@ -457,10 +465,11 @@ def moe_route_topk_backward(topk_idx: torch.Tensor, topk_w: torch.Tensor, d_topk
         raise ValueError("renormalize=False needs the logits")
     own = []
     if d_logits is None:
-        d_logits = torch.empty((n, n_experts), dtype=torch.float32, device=dev)
+        d_logits = topk_w.new_empty((n, n_experts))
         own.append(d_logits)
-    _need(d_logits, "d_logits", (torch.float32,), dev)
-    _shape(d_logits, "d_logits", (n, n_experts))
+    else:
+        _need(d_logits, "d_logits", (torch.float32,), dev)
+        _shape(d_logits, "d_logits", (n, n_experts))
     _launch("moe_route_topk_backward", dev, stream,
             (_ptr(logits), _ptr(topk_idx), _ptr(topk_w), _ptr(d_topk_w), n, n_experts, k,
              int(bool(renormalize)), _ptr(d_logits)), own)
@@ -642,13 +651,17 @@ def moe_quantize_mxfp4(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
     r, k = x.shape
     own = []
     if codes is None:
-        codes = torch.empty((r, k // 2), dtype=torch.uint8, device=dev)
+        codes = x.new_empty((r, k // 2), dtype=torch.uint8)
         own.append(codes)
+    else:
+        _need(codes, "codes", (torch.uint8,), dev)
+        _shape(codes, "codes", (r, k // 2))
     if scales is None:
-        scales = torch.empty((r, k // 32), dtype=torch.uint8, device=dev)
+        scales = x.new_empty((r, k // 32), dtype=torch.uint8)
         own.append(scales)
-    _mxfp4_operand(codes, scales, "codes", 2, dev)
-    _shape(codes, "codes", (r, k // 2))
+    else:
+        _need(scales, "scales", (torch.uint8,), dev)
+        _shape(scales, "scales", (r, k // 32))
     _launch("moe_quantize_mxfp4", dev, stream,
             (_ptr(x), _FLOAT_IO[x.dtype], r, k, _ptr(codes), _ptr(scales)), own)
     return codes, scales
@@ -663,10 +676,13 @@ def moe_dequant_mxfp4(codes: torch.Tensor, scales: torch.Tensor,
     r, k = codes.shape[0], codes.shape[1] * 2
     own = []
     if out is None:
-        out = torch.empty((r, k), dtype=out_dtype, device=dev)
+        out = codes.new_empty((r, k), dtype=out_dtype)
         own.append(out)
-    _need(out, "out", tuple(_FLOAT_IO), dev)
-    _shape(out, "out", (r, k))
+        if out_dtype not in _FLOAT_IO:
+            raise TypeError(f"out_dtype is {out_dtype}, expected one of {tuple(_FLOAT_IO)}")
+    else:
+        _need(out, "out", tuple(_FLOAT_IO), dev)
+        _shape(out, "out", (r, k))
     _launch("moe_dequant_mxfp4", dev, stream,
             (_ptr(codes), _ptr(scales), r, k, _ptr(out), _FLOAT_IO[out.dtype]), own)
     return out
@@ -690,10 +706,11 @@ def _mxfp4_product(fn, rows, row_scales, index, n_index, w, w_scales, w_up, w_up
         raise ValueError(f"{fn}: expert_offsets must be [E+1], row_expert [R]")
     own = []
     if y is None:
-        y = torch.empty((rows.shape[0], n), dtype=torch.bfloat16, device=dev)
+        y = rows.new_empty((rows.shape[0], n), dtype=torch.bfloat16)
         own.append(y)
-    _need(y, "y", (torch.bfloat16,), dev)
-    _shape(y, "y", (rows.shape[0], n))
+    else:
+        _need(y, "y", (torch.bfloat16,), dev)
+        _shape(y, "y", (rows.shape[0], n))
     return dev, e, n, 2 * kh, y, own
 
 
@@ -729,10 +746,10 @@ def moe_gather_gemm_mxfp4(rows: torch.Tensor, row_scales: torch.Tensor, row_expe
     dev, e, n, k, y, own = _mxfp4_product("moe_gather_gemm_mxfp4", rows, row_scales, row_expert,
                                           rows.shape[0], w, w_scales, w_up, w_up_scales, y)
     if workspace is None:
-        workspace = torch.empty(max(moe_gather_gemm_mxfp4_workspace_bytes(rows.shape[0], e), 256),
-                                dtype=torch.uint8, device=dev)
+        workspace = rows.new_empty(max(moe_gather_gemm_mxfp4_workspace_bytes(rows.shape[0], e), 256))
         own.append(workspace)
-    _need(workspace, "workspace", (torch.uint8,), dev)
+    else:
+        _need(workspace, "workspace", (torch.uint8,), dev)
     _launch("moe_gather_gemm_mxfp4", dev, stream,
             (_ptr(rows), _ptr(row_scales), rows.shape[0], k, _ptr(row_expert), e, _ptr(w),
              _ptr(w_scales), _ptr(w_up), _ptr(w_up_scales), n, _ptr(y), _ptr(workspace),

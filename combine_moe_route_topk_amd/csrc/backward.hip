@@ -16,9 +16,9 @@ namespace {
 
 constexpr int kBlock = 256;
 constexpr int kWaves = kBlock / kWave;
-constexpr int kGroup = 8;          // elements per lane per load group
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
@@ -29,58 +29,77 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
-// 8 consecutive elements of a row in registers as loaded.
-template <typename T> struct Raw;
-template <> struct Raw<uint16_t> {
+__device__ __forceinline__ uint32_t pack2(float a, float b) {   // rounds to nearest even
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+
+template <bool NT, typename V>
+__device__ __forceinline__ V load_as(const void* p) {
+  return NT ? __builtin_nontemporal_load(static_cast<const V*>(p)) : *static_cast<const V*>(p);
+}
+
+// G consecutive elements of a row in registers as loaded.
+template <typename T, int G> struct Raw;
+template <> struct Raw<uint16_t, 8> {
   u32x4 v;
-  template <bool NT> __device__ void load(const uint16_t* p) {
-    v = NT ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p))
-           : *reinterpret_cast<const u32x4*>(p);
+  template <bool NT> __device__ void load(const uint16_t* p) { v = load_as<NT, u32x4>(p); }
+  __device__ void to_f32(float (&o)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack_bf16x2(v[i], o[2 * i], o[2 * i + 1]);
   }
-  __device__ void to_f32(float (&o)[kGroup]) const {
+  __device__ static void store(uint16_t* p, const float (&o)[8]) {
+    __builtin_nontemporal_store(u32x4{pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]),
+                                      pack2(o[6], o[7])}, reinterpret_cast<u32x4*>(p));
+  }
+};
+template <> struct Raw<uint16_t, 4> {
+  u32x2 v;
+  template <bool NT> __device__ void load(const uint16_t* p) { v = load_as<NT, u32x2>(p); }
+  __device__ void to_f32(float (&o)[4]) const {
     unpack_bf16x2(v.x, o[0], o[1]); unpack_bf16x2(v.y, o[2], o[3]);
-    unpack_bf16x2(v.z, o[4], o[5]); unpack_bf16x2(v.w, o[6], o[7]);
   }
-  __device__ static uint32_t pack(float a, float b) {   // rounds to nearest even
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
-  }
-  __device__ static void store(uint16_t* p, const float (&o)[kGroup]) {
-    const u32x4 r = {pack(o[0], o[1]), pack(o[2], o[3]), pack(o[4], o[5]), pack(o[6], o[7])};
-    __builtin_nontemporal_store(r, reinterpret_cast<u32x4*>(p));
+  __device__ static void store(uint16_t* p, const float (&o)[4]) {
+    __builtin_nontemporal_store(u32x2{pack2(o[0], o[1]), pack2(o[2], o[3])}, reinterpret_cast<u32x2*>(p));
   }
 };
-template <> struct Raw<float> {
-  u32x4 a, b;
+template <> struct Raw<uint16_t, 1> {
+  uint16_t v;
+  template <bool NT> __device__ void load(const uint16_t* p) { v = load_as<NT, uint16_t>(p); }
+  __device__ void to_f32(float (&o)[1]) const { o[0] = bf16_to_f32(v); }
+  __device__ static void store(uint16_t* p, const float (&o)[1]) { *p = f32_to_bf16_rne(o[0]); }
+};
+template <int G> struct Raw<float, G> {       // 4 or 8
+  u32x4 v[G / 4];
   template <bool NT> __device__ void load(const float* p) {
-    const u32x4* q = reinterpret_cast<const u32x4*>(p);
-    a = NT ? __builtin_nontemporal_load(q) : q[0];
-    b = NT ? __builtin_nontemporal_load(q + 1) : q[1];
+#pragma unroll
+    for (int i = 0; i < G / 4; ++i) v[i] = load_as<NT, u32x4>(p + 4 * i);
   }
-  __device__ void to_f32(float (&o)[kGroup]) const {
-    o[0] = __uint_as_float(a.x); o[1] = __uint_as_float(a.y);
-    o[2] = __uint_as_float(a.z); o[3] = __uint_as_float(a.w);
-    o[4] = __uint_as_float(b.x); o[5] = __uint_as_float(b.y);
-    o[6] = __uint_as_float(b.z); o[7] = __uint_as_float(b.w);
+  __device__ void to_f32(float (&o)[G]) const {
+#pragma unroll
+    for (int i = 0; i < G; ++i) o[i] = __uint_as_float(v[i / 4][i % 4]);
   }
-  __device__ static void store(float* p, const float (&o)[kGroup]) {
-    u32x4* q = reinterpret_cast<u32x4*>(p);
-    __builtin_nontemporal_store(u32x4{__float_as_uint(o[0]), __float_as_uint(o[1]),
-                                      __float_as_uint(o[2]), __float_as_uint(o[3])}, q);
-    __builtin_nontemporal_store(u32x4{__float_as_uint(o[4]), __float_as_uint(o[5]),
-                                      __float_as_uint(o[6]), __float_as_uint(o[7])}, q + 1);
+  __device__ static void store(float* p, const float (&o)[G]) {
+#pragma unroll
+    for (int i = 0; i < G / 4; ++i)
+      __builtin_nontemporal_store(u32x4{__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
+                                        __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3])},
+                                  reinterpret_cast<u32x4*>(p + 4 * i));
   }
 };
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
-__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store1(uint16_t* p, float v) { *p = f32_to_bf16_rne(v); }
+template <> struct Raw<float, 1> {
+  float v;
+  template <bool NT> __device__ void load(const float* p) { v = load_as<NT, float>(p); }
+  __device__ void to_f32(float (&o)[1]) const { o[0] = v; }
+  __device__ static void store(float* p, const float (&o)[1]) { *p = o[0]; }
+};
 
 // One wave per pair q = t*k + j: it reads row dst_pos[q] of y and row t of
 // d_out once, writes row dst_pos[q] of d_y, and keeps the dot product in fp32
 // registers, so d_w needs no second pass, no atomics and no workspace.  The k
 // waves of a token sit side by side, so d_out comes from the caches after the
 // first.  y and d_y are touched once and bypass them (non-temporal).
-template <typename TG, typename TY, int U>
+// Lanes take G consecutive elements at a time, U groups in flight.
+template <typename TG, typename TY, int G, int U>
 __global__ __launch_bounds__(kBlock) void combine_backward_kernel(
     const TG* __restrict__ d_out, const TY* __restrict__ y, int64_t nk, int64_t hidden, int k,
     const int32_t* __restrict__ dst_pos, const float* __restrict__ topk_w, TY* __restrict__ d_y,
@@ -98,58 +117,31 @@ __global__ __launch_bounds__(kBlock) void combine_backward_kernel(
   const TY* yr = y + int64_t(p) * hidden;
   TY* dr = d_y + int64_t(p) * hidden;
   float dot = 0.f;
-  const int64_t ngroups = hidden / kGroup;
+  const int64_t ngroups = hidden / G;
   for (int64_t g0 = lane; g0 < ngroups; g0 += U * kWave) {
-    Raw<TG> rg[U];
-    Raw<TY> ry[U];
+    Raw<TG, G> rg[U];
+    Raw<TY, G> ry[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       // past the row's end: its last group again, not used
       const int64_t gi = g0 + u * kWave < ngroups ? g0 + u * kWave : ngroups - 1;
-      ry[u].template load<true>(yr + gi * kGroup);
-      rg[u].template load<false>(g + gi * kGroup);
+      ry[u].template load<true>(yr + gi * G);
+      rg[u].template load<false>(g + gi * G);
     }
+    __builtin_amdgcn_sched_barrier(0);          // all loads go out before the first is used
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (g0 + u * kWave >= ngroups) break;
-      float a[kGroup], b[kGroup];
+      float a[G], b[G];
       rg[u].to_f32(a);
       ry[u].to_f32(b);
 #pragma unroll
-      for (int i = 0; i < kGroup; ++i) {
+      for (int i = 0; i < G; ++i) {
         dot = __builtin_fmaf(a[i], b[i], dot);
         a[i] *= w;
       }
-      Raw<TY>::store(dr + (g0 + u * kWave) * kGroup, a);
+      Raw<TY, G>::store(dr + (g0 + u * kWave) * G, a);
     }
-  }
-  dot = wave_sum(dot);
-  if (lane == 0) d_w[q] = dot;
-}
-
-// Any D and alignment: one element per lane.
-template <typename TG, typename TY>
-__global__ __launch_bounds__(kBlock) void combine_backward_scalar_kernel(
-    const TG* __restrict__ d_out, const TY* __restrict__ y, int64_t nk, int64_t hidden, int k,
-    const int32_t* __restrict__ dst_pos, const float* __restrict__ topk_w, TY* __restrict__ d_y,
-    float* __restrict__ d_w) {
-  const int lane = lane_id();
-  const int64_t q = int64_t(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(int(threadIdx.x / kWave));
-  if (q >= nk) return;
-  const int p = __builtin_amdgcn_readfirstlane(dst_pos[q]);
-  if (unsigned(p) >= uint64_t(nk)) {
-    if (lane == 0) d_w[q] = 0.f;
-    return;
-  }
-  const float w = topk_w[q];
-  const TG* g = d_out + q / k * hidden;
-  const TY* yr = y + int64_t(p) * hidden;
-  TY* dr = d_y + int64_t(p) * hidden;
-  float dot = 0.f;
-  for (int64_t i = lane; i < hidden; i += kWave) {
-    const float a = load1(g + i);
-    dot = __builtin_fmaf(a, load1(yr + i), dot);
-    store1(dr + i, w * a);
   }
   dot = wave_sum(dot);
   if (lane == 0) d_w[q] = dot;
@@ -162,17 +154,23 @@ hipError_t launch_combine_backward_typed(const void* d_out, const void* y, int64
                                          hipStream_t stream) {
   const int64_t nk = n_tokens * k;
   const unsigned blocks = unsigned((nk + kWaves - 1) / kWaves);
-  const bool aligned = ((reinterpret_cast<uintptr_t>(d_out) | reinterpret_cast<uintptr_t>(y) |
-                         reinterpret_cast<uintptr_t>(d_y)) & 15) == 0;
   const TG* g = static_cast<const TG*>(d_out);
   const TY* yy = static_cast<const TY*>(y);
   TY* dy = static_cast<TY*>(d_y);
-  if (aligned && hidden % kGroup == 0)
-    combine_backward_kernel<TG, TY, 4><<<blocks, kBlock, 0, stream>>>(g, yy, nk, hidden, k, dst_pos,
-                                                                      topk_w, dy, d_w);
+  // groups of G start on the alignment of their widest load (16 bytes at most)
+  auto fits = [&](int64_t n) {
+    auto ok = [&](const void* p, size_t elem) {
+      const size_t a = n * elem < 16 ? n * elem : 16;
+      return reinterpret_cast<uintptr_t>(p) % a == 0;
+    };
+    return hidden % n == 0 && ok(g, sizeof(TG)) && ok(yy, sizeof(TY)) && ok(dy, sizeof(TY));
+  };
+  if (fits(8))
+    combine_backward_kernel<TG, TY, 8, 4><<<blocks, kBlock, 0, stream>>>(g, yy, nk, hidden, k, dst_pos, topk_w, dy, d_w);
+  else if (fits(4))
+    combine_backward_kernel<TG, TY, 4, 4><<<blocks, kBlock, 0, stream>>>(g, yy, nk, hidden, k, dst_pos, topk_w, dy, d_w);
   else
-    combine_backward_scalar_kernel<TG, TY><<<blocks, kBlock, 0, stream>>>(g, yy, nk, hidden, k,
-                                                                          dst_pos, topk_w, dy, d_w);
+    combine_backward_kernel<TG, TY, 1, 8><<<blocks, kBlock, 0, stream>>>(g, yy, nk, hidden, k, dst_pos, topk_w, dy, d_w);
   return hipGetLastError();
 }
 

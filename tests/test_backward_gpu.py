@@ -207,6 +207,8 @@ def test_backward_refusals():
         moe.moe_dispatch_backward(t(8, 64), pos, 3)
     with pytest.raises(ValueError):
         moe.moe_dispatch_backward(t(8, 64), pos, 2, d_x=t(3, 64))
+    with pytest.raises(TypeError):
+        moe.moe_dispatch_backward(t(8, 64), pos, 2, out_dtype=torch.float16)
     with pytest.raises(ValueError):
         moe.moe_route_topk_backward(t(4, 2, dt=torch.int32), w, w, 8, renormalize=False)
     with pytest.raises(ValueError):

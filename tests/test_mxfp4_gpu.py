@@ -306,7 +306,11 @@ def test_refusals():
     with pytest.raises(ValueError):
         moe.moe_quantize_mxfp4(f(4, 128)[:, ::2])
     with pytest.raises(ValueError):
+        moe.moe_quantize_mxfp4(f(4, 64), scales=z(4, 3))
+    with pytest.raises(ValueError):
         moe.moe_dequant_mxfp4(z(4, 32), z(4, 3))
+    with pytest.raises(TypeError):
+        moe.moe_dequant_mxfp4(z(4, 32), z(4, 2), out_dtype=torch.float16)
     for fn, idx in ((moe.moe_grouped_gemm_mxfp4, i32(3)), (moe.moe_gather_gemm_mxfp4, i32(4))):
         ok = (z(4, 64), z(4, 4), idx, z(2, 8, 64), z(2, 8, 4))
         fn(*ok)
