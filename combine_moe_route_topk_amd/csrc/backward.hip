@@ -97,19 +97,26 @@ template <> struct Raw<float, 1> {
 // d_out once, writes row dst_pos[q] of d_y, and keeps the dot product in fp32
 // registers, so d_w needs no second pass, no atomics and no workspace.  The k
 // waves of a token sit side by side, so d_out comes from the caches after the
-// first.  y and d_y are touched once and bypass them (non-temporal).
-// Lanes take G consecutive elements at a time, U groups in flight.
-template <typename TG, typename TY, int G, int U>
+// first.  y and d_y are touched once and bypass them (non-temporal).  Bound by
+// memory: 4096 tokens x 7168, top-8, bf16 move 1 GB in 183 us, 5.5 TB/s (a
+// device copy reaches 4.8 here).
+// Lanes take G consecutive elements at a time, U groups in flight.  WPP: waves
+// per pair, which share its row and add their partial sums in wave order.
+template <typename TG, typename TY, int G, int U, int WPP>
 __global__ __launch_bounds__(kBlock) void combine_backward_kernel(
     const TG* __restrict__ d_out, const TY* __restrict__ y, int64_t nk, int64_t hidden, int k,
     const int32_t* __restrict__ dst_pos, const float* __restrict__ topk_w, TY* __restrict__ d_y,
     float* __restrict__ d_w) {
+  static_assert(WPP == 1 || WPP == kWaves, "a wave or a workgroup per pair");
+  __shared__ float s_part[kWaves];
   const int lane = lane_id();
-  const int64_t q = int64_t(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(int(threadIdx.x / kWave));
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x / kWave));
+  const int64_t q = WPP == 1 ? int64_t(blockIdx.x) * kWaves + wave : int64_t(blockIdx.x);
   if (q >= nk) return;
   const int p = __builtin_amdgcn_readfirstlane(dst_pos[q]);
+  const bool writes = lane == 0 && (WPP == 1 || wave == 0);
   if (unsigned(p) >= uint64_t(nk)) {            // a pair that holds no row
-    if (lane == 0) d_w[q] = 0.f;
+    if (writes) d_w[q] = 0.f;
     return;
   }
   const float w = topk_w[q];
@@ -118,7 +125,7 @@ __global__ __launch_bounds__(kBlock) void combine_backward_kernel(
   TY* dr = d_y + int64_t(p) * hidden;
   float dot = 0.f;
   const int64_t ngroups = hidden / G;
-  for (int64_t g0 = lane; g0 < ngroups; g0 += U * kWave) {
+  for (int64_t g0 = (WPP == 1 ? 0 : wave * U * kWave) + lane; g0 < ngroups; g0 += WPP * U * kWave) {
     Raw<TG, G> rg[U];
     Raw<TY, G> ry[U];
 #pragma unroll
@@ -144,7 +151,14 @@ __global__ __launch_bounds__(kBlock) void combine_backward_kernel(
     }
   }
   dot = wave_sum(dot);
-  if (lane == 0) d_w[q] = dot;
+  if (WPP > 1) {
+    if (lane == 0) s_part[wave] = dot;
+    __syncthreads();
+    dot = s_part[0];
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i) dot += s_part[i];
+  }
+  if (writes) d_w[q] = dot;
 }
 
 template <typename TG, typename TY>
@@ -153,7 +167,6 @@ hipError_t launch_combine_backward_typed(const void* d_out, const void* y, int64
                                          const float* topk_w, void* d_y, float* d_w,
                                          hipStream_t stream) {
   const int64_t nk = n_tokens * k;
-  const unsigned blocks = unsigned((nk + kWaves - 1) / kWaves);
   const TG* g = static_cast<const TG*>(d_out);
   const TY* yy = static_cast<const TY*>(y);
   TY* dy = static_cast<TY*>(d_y);
@@ -165,12 +178,17 @@ hipError_t launch_combine_backward_typed(const void* d_out, const void* y, int64
     };
     return hidden % n == 0 && ok(g, sizeof(TG)) && ok(yy, sizeof(TY)) && ok(dy, sizeof(TY));
   };
-  if (fits(8))
-    combine_backward_kernel<TG, TY, 8, 4><<<blocks, kBlock, 0, stream>>>(g, yy, nk, hidden, k, dst_pos, topk_w, dy, d_w);
-  else if (fits(4))
-    combine_backward_kernel<TG, TY, 4, 4><<<blocks, kBlock, 0, stream>>>(g, yy, nk, hidden, k, dst_pos, topk_w, dy, d_w);
-  else
-    combine_backward_kernel<TG, TY, 1, 8><<<blocks, kBlock, 0, stream>>>(g, yy, nk, hidden, k, dst_pos, topk_w, dy, d_w);
+  auto run = [&](auto kernel, int per_block) {
+    kernel<<<unsigned((nk + per_block - 1) / per_block), kBlock, 0, stream>>>(g, yy, nk, hidden, k, dst_pos, topk_w, dy, d_w);
+  };
+  // a workgroup per pair where a wave per pair would leave the card idle and
+  // rows are long enough to share.  Measured, wave against workgroup per pair:
+  // 1024 pairs of 7168 bf16 14.8 and 8.8 us, 2048 of 4096 12.5 and 9.8; 4096 of
+  // 7168 25.6 and 28.6, 2800 of 1001 5.3 and 6.0.
+  const bool few = nk < 4096 && hidden >= 2048;
+  if (fits(8)) few ? run(combine_backward_kernel<TG, TY, 8, 4, kWaves>, 1) : run(combine_backward_kernel<TG, TY, 8, 4, 1>, kWaves);
+  else if (fits(4)) few ? run(combine_backward_kernel<TG, TY, 4, 4, kWaves>, 1) : run(combine_backward_kernel<TG, TY, 4, 4, 1>, kWaves);
+  else few ? run(combine_backward_kernel<TG, TY, 1, 8, kWaves>, 1) : run(combine_backward_kernel<TG, TY, 1, 8, 1>, kWaves);
   return hipGetLastError();
 }
 
