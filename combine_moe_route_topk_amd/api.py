@@ -9,6 +9,7 @@ computes.
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 from typing import Optional
 
@@ -27,8 +28,8 @@ __all__ = ["moe_route_topk", "moe_resolve_sorted", "default_sort_cutoff", "moe_d
            "MoeError"]
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream) -> ctypes.c_void_p:
@@ -631,12 +632,15 @@ def moe_grouped_gemm_fp8(rows: torch.Tensor, row_scales: torch.Tensor, expert_of
     return y
 
 
-def _mxfp4_operand(codes: torch.Tensor, scales: torch.Tensor, name: str, dims: int, dev=None) -> None:
+def _mxfp4_operand(codes: torch.Tensor, scales: torch.Tensor, name: str, scales_name: str, dims: int,
+                   dev=None) -> None:
     _need(codes, name, (torch.uint8,), dev)
-    _need(scales, f"{name}'s scales", (torch.uint8,), codes.device)
-    if codes.dim() != dims or codes.shape[-1] % 16:
+    _need(scales, scales_name, (torch.uint8,), codes.device)
+    cs, ss = codes.shape, scales.shape
+    if len(cs) != dims or cs[-1] % 16:
         raise ValueError(f"{name} must have {dims} dimensions, the last K/2 with K % 32 == 0")
-    _shape(scales, f"{name}'s scales", tuple(codes.shape[:-1]) + (codes.shape[-1] // 16,))
+    if len(ss) != dims or ss[:-1] != cs[:-1] or ss[-1] * 16 != cs[-1]:
+        raise ValueError(f"{scales_name} has shape {tuple(ss)}, expected {tuple(cs[:-1]) + (cs[-1] // 16,)}")
 
 
 def moe_quantize_mxfp4(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
@@ -671,7 +675,7 @@ def moe_dequant_mxfp4(codes: torch.Tensor, scales: torch.Tensor,
                       out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
                       stream=None) -> torch.Tensor:
     """MXFP4 codes [R, K/2] and scales [R, K/32] -> their values [R, K]."""
-    _mxfp4_operand(codes, scales, "codes", 2)
+    _mxfp4_operand(codes, scales, "codes", "scales", 2)
     dev = codes.device
     r, k = codes.shape[0], codes.shape[1] * 2
     own = []
@@ -690,19 +694,19 @@ def moe_dequant_mxfp4(codes: torch.Tensor, scales: torch.Tensor,
 
 def _mxfp4_product(fn, rows, row_scales, index, n_index, w, w_scales, w_up, w_up_scales, y):
     """Shared checks of the two MXFP4 products -> (device, sizes, y, own)."""
-    _mxfp4_operand(rows, row_scales, "rows", 2)
+    _mxfp4_operand(rows, row_scales, "rows", "row_scales", 2)
     dev = rows.device
-    _mxfp4_operand(w, w_scales, "w", 3, dev)
+    _mxfp4_operand(w, w_scales, "w", "w_scales", 3, dev)
     if (w_up is None) != (w_up_scales is None):
         raise ValueError(f"{fn}: w_up and w_up_scales go together")
     if w_up is not None:
-        _mxfp4_operand(w_up, w_up_scales, "w_up", 3, dev)
+        _mxfp4_operand(w_up, w_up_scales, "w_up", "w_up_scales", 3, dev)
         _shape(w_up, "w_up", w.shape)
     e, n, kh = w.shape
     if rows.shape[1] != kh:
         raise ValueError(f"{fn}: rows have {rows.shape[1]} code bytes, w {kh}")
     _need(index, "expert_offsets / row_expert", (torch.int32,), dev)
-    if index.numel() != (e + 1 if n_index is None else n_index):
+    if index.dim() != 1 or index.shape[0] != (e + 1 if n_index is None else n_index):
         raise ValueError(f"{fn}: expert_offsets must be [E+1], row_expert [R]")
     own = []
     if y is None:
@@ -731,6 +735,7 @@ def moe_grouped_gemm_mxfp4(rows: torch.Tensor, row_scales: torch.Tensor,
     return y
 
 
+@functools.lru_cache(maxsize=1024)        # a function of the sizes alone
 def moe_gather_gemm_mxfp4_workspace_bytes(n_rows: int, n_experts: int) -> int:
     return int(lib.moe_gather_gemm_mxfp4_workspace_bytes(n_rows, n_experts))
 
