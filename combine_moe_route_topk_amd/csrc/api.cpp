@@ -630,7 +630,7 @@ int check_mxfp4_rows(const char* fn, int32_t dtype, int64_t n_rows, int64_t k_di
   return MOE_OK;
 }
 
-int check_mxfp4_product(const char* fn, const moe::Mxfp4Product& g, const void* index) {
+int check_mxfp4_product(const char* fn, const moe::Mxfp4Product& g, const void* index, bool gather) {
   if (g.n_rows < 0) return fail(MOE_ERR_ARG, "%s: n_rows < 0", fn);
   if (g.k_dim < 1 || g.n_dim < 1 || g.n_experts < 1) return fail(MOE_ERR_ARG, "%s: sizes must be >= 1", fn);
   if (!g.w_up != !g.w_up_scales)
@@ -641,7 +641,7 @@ int check_mxfp4_product(const char* fn, const moe::Mxfp4Product& g, const void* 
   if (g.k_dim > (int64_t(1) << 22) || g.n_dim > (int64_t(1) << 22))
     return fail(MOE_ERR_UNSUPPORTED, "%s: k_dim and n_dim must be at most %d", fn, 1 << 22);
   if (g.n_rows > INT32_MAX) return fail(MOE_ERR_UNSUPPORTED, "%s: n_rows exceeds the int32 range", fn);
-  if (moe::gemm_mxfp4_tiles(g.n_rows, g.n_experts, g.n_dim) > INT32_MAX - 8)
+  if (g.n_rows > 0 && moe::gemm_mxfp4_blocks(g, gather) > moe::kMaxMxfp4Blocks)
     return fail(MOE_ERR_UNSUPPORTED, "%s: too many tiles", fn);
   if (g.n_rows == 0) return MOE_OK;
   if (!g.rows || !g.row_scales || !index || !g.w || !g.w_scales || !g.y)
@@ -689,7 +689,7 @@ int moe_grouped_gemm_mxfp4(const uint8_t* rows, const uint8_t* row_scales, int64
   const char* fn = "moe_grouped_gemm_mxfp4";
   const moe::Mxfp4Product g{rows, row_scales, n_rows, k_dim, n_experts, w, w_scales,
                             w_up, w_up_scales, n_dim, y};
-  const int rc = check_mxfp4_product(fn, g, expert_offsets);
+  const int rc = check_mxfp4_product(fn, g, expert_offsets, false);
   if (rc) return rc;
   if (n_rows == 0) return ok();
   return hip_status(moe::launch_grouped_gemm_mxfp4(g, expert_offsets, static_cast<hipStream_t>(stream)),
@@ -709,7 +709,7 @@ int moe_gather_gemm_mxfp4(const uint8_t* rows, const uint8_t* row_scales, int64_
   const char* fn = "moe_gather_gemm_mxfp4";
   const moe::Mxfp4Product g{rows, row_scales, n_rows, k_dim, n_experts, w, w_scales,
                             w_up, w_up_scales, n_dim, y};
-  const int rc = check_mxfp4_product(fn, g, row_expert);
+  const int rc = check_mxfp4_product(fn, g, row_expert, true);
   if (rc) return rc;
   if (n_rows == 0) return ok();
   const size_t need = moe::gather_gemm_mxfp4_workspace_bytes(n_rows, n_experts);

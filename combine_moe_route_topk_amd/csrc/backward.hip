@@ -111,7 +111,7 @@ __global__ __launch_bounds__(kBlock) void combine_backward_kernel(
   __shared__ float s_part[kWaves];
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x / kWave));
-  const int64_t q = WPP == 1 ? int64_t(blockIdx.x) * kWaves + wave : int64_t(blockIdx.x);
+  const int64_t q = WPP == 1 ? block_id() * kWaves + wave : block_id();
   if (q >= nk) return;
   const int p = __builtin_amdgcn_readfirstlane(dst_pos[q]);
   const bool writes = lane == 0 && (WPP == 1 || wave == 0);
@@ -179,7 +179,7 @@ hipError_t launch_combine_backward_typed(const void* d_out, const void* y, int64
     return hidden % n == 0 && ok(g, sizeof(TG)) && ok(yy, sizeof(TY)) && ok(dy, sizeof(TY));
   };
   auto run = [&](auto kernel, int per_block) {
-    kernel<<<unsigned((nk + per_block - 1) / per_block), kBlock, 0, stream>>>(g, yy, nk, hidden, k, dst_pos, topk_w, dy, d_w);
+    kernel<<<grid_of((nk + per_block - 1) / per_block), kBlock, 0, stream>>>(g, yy, nk, hidden, k, dst_pos, topk_w, dy, d_w);
   };
   // a workgroup per pair where a wave per pair would leave the card idle and
   // rows are long enough to share.  Measured, wave against workgroup per pair:
@@ -203,7 +203,7 @@ __global__ __launch_bounds__(kBlock) void route_backward_kernel(
     const float* __restrict__ topk_w, const float* __restrict__ d_w, int64_t n_tokens,
     int n_experts, int k, float* __restrict__ d_logits) {
   const int lane = lane_id();
-  const int64_t t = int64_t(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(int(threadIdx.x / kWave));
+  const int64_t t = block_id() * kWaves + __builtin_amdgcn_readfirstlane(int(threadIdx.x / kWave));
   if (t >= n_tokens) return;
   const bool has = lane < k;
   const int my_e = has ? topk_idx[t * k + lane] : -1;
@@ -246,7 +246,7 @@ template <bool RENORM>
 void launch_route_backward_slots(const float* logits, const int32_t* idx, const float* w,
                                  const float* d_w, int64_t n, int e, int k, float* d_logits,
                                  hipStream_t stream) {
-  const unsigned blocks = unsigned((n + kWaves - 1) / kWaves);
+  const dim3 blocks = grid_of((n + kWaves - 1) / kWaves);
   if (e <= 64)
     route_backward_kernel<1, RENORM><<<blocks, kBlock, 0, stream>>>(logits, idx, w, d_w, n, e, k, d_logits);
   else if (e <= 128)

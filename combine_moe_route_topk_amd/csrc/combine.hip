@@ -13,6 +13,8 @@
 // FMA chain acc = fma(w_j, y_j, acc) in slot order j = 0..k-1.  The order
 // never depends on where dispatch put the rows, so sorted and unsorted
 // layouts give bit-identical outputs.  Rounding to bf16 is nearest-even.
+#include <algorithm>
+
 #include "device_common.hpp"
 #include "launch.hpp"
 
@@ -191,10 +193,9 @@ __global__ __launch_bounds__(kBlock) void combine_scalar_kernel(
 }
 
 template <typename TY, typename TO, bool W>
-hipError_t launch_combine_typed(const void* y, int64_t n_tokens, int64_t hidden, int k,
+hipError_t launch_combine_typed(const void* y, int64_t nk, int64_t n_tokens, int64_t hidden, int k,
                                 const int32_t* dst_pos, const float* topk_w, void* out,
                                 hipStream_t stream) {
-  const int64_t nk = n_tokens * k;
   const int per_block = kBlock / kWave;
   const bool aligned = ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(out)) & 15) == 0;
   // Fewer than 4096 two-kilobyte items (decode-sized batches): 1 KB slices
@@ -300,13 +301,27 @@ template <bool W>
 hipError_t launch_combine_any(const void* y, int y_bf16, int64_t n_tokens, int64_t hidden, int k,
                               const int32_t* dst_pos, const float* topk_w, void* out, int out_bf16,
                               hipStream_t stream) {
-  if (y_bf16 && out_bf16)
-    return launch_combine_typed<uint16_t, uint16_t, W>(y, n_tokens, hidden, k, dst_pos, topk_w, out, stream);
-  if (y_bf16)
-    return launch_combine_typed<uint16_t, float, W>(y, n_tokens, hidden, k, dst_pos, topk_w, out, stream);
-  if (out_bf16)
-    return launch_combine_typed<float, uint16_t, W>(y, n_tokens, hidden, k, dst_pos, topk_w, out, stream);
-  return launch_combine_typed<float, float, W>(y, n_tokens, hidden, k, dst_pos, topk_w, out, stream);
+  // a launch holds fewer than 2^32 threads: tokens beyond take another one (a
+  // wave per token and 64 elements at most)
+  const int64_t most = std::max<int64_t>(1, ((int64_t(1) << 26) - 4) / ((hidden + kWave - 1) / kWave));
+  const int64_t nk = n_tokens * k;
+  for (int64_t t = 0; t < n_tokens; t += most) {
+    const int64_t n = std::min(most, n_tokens - t);
+    const int32_t* pos = dst_pos + t * k;
+    const float* w = W ? topk_w + t * k : nullptr;
+    void* o = static_cast<char*>(out) + t * hidden * (out_bf16 ? 2 : 4);
+    hipError_t err;
+    if (y_bf16 && out_bf16)
+      err = launch_combine_typed<uint16_t, uint16_t, W>(y, nk, n, hidden, k, pos, w, o, stream);
+    else if (y_bf16)
+      err = launch_combine_typed<uint16_t, float, W>(y, nk, n, hidden, k, pos, w, o, stream);
+    else if (out_bf16)
+      err = launch_combine_typed<float, uint16_t, W>(y, nk, n, hidden, k, pos, w, o, stream);
+    else
+      err = launch_combine_typed<float, float, W>(y, nk, n, hidden, k, pos, w, o, stream);
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 }  // namespace

@@ -17,6 +17,11 @@ __device__ __forceinline__ uint64_t lanemask_lt() {
 
 __device__ __forceinline__ uint64_t ballot(bool p) { return __ballot(p); }
 
+// Number of this workgroup in a grid made by grid_of().
+__device__ __forceinline__ int64_t block_id() {
+  return int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
+}
+
 // bfloat16 <-> float32.  Decoding is exact; encoding rounds to nearest even and
 // keeps NaN quiet.
 __device__ __forceinline__ float bf16_to_f32(uint16_t b) {

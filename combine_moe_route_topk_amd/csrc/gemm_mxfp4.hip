@@ -63,7 +63,8 @@ __device__ Tile find_tile(int m_idx, const int32_t* __restrict__ offs, int n_exp
 
 // silu(a) = a / (1 + e^-a) from the exponential and reciprocal instructions (1
 // ulp each): about 2^-21 off, beside the 2^-8 of the bf16 rounding that follows.
-// a = -inf gives NaN as a / (1 + e^-a) does.
+// Below -87 the result is 0 (a e^a, under 2^-119, is lost with the reciprocal's
+// subnormals); -inf gives NaN, as a / (1 + e^-a) does.
 __device__ __forceinline__ float silu(float a) {
   return a * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(a * -1.44269504f));
 }
@@ -91,7 +92,7 @@ __device__ __forceinline__ void store4(uint16_t* row, int c, int n, bool whole, 
 // ---------------------------------------------------------------- few rows per expert
 // The weights are most of the bytes: each is read once per tile of 16 NB rows,
 // straight from memory into registers, 1024 elements of K of every weight row
-// in flight.  A workgroup of 8 waves takes one tile; a wave owns 32 weight rows
+// in flight.  A workgroup of 4 waves takes one tile; a wave owns 32 weight rows
 // (SwiGLU: 16 of w and the same 16 of w_up, so silu(g) * u is lane-local) over
 // the whole K, as the A operand of v_mfma_scale_f32_16x16x128: lane (n, g) =
 // (l % 16, l / 16) holds row n and block 4 s + g of step s, so one load
@@ -105,7 +106,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x4a __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr int kWT = 2;                   // 16-row weight tiles per wave
-constexpr int kCh = 4;                   // K steps of 128 per chunk
+constexpr int kCh = 4;                   // K steps of 128 per refill
 constexpr int kSt = 8;                   // K steps per LDS stage (1024 elements), all in flight
 constexpr int kPitch = kSt * 64 + 16;    // code bytes of a staged row: rows land 4 banks apart
 constexpr int kScPitch = kSt * 4 + 16;   // scale bytes of a staged row
@@ -715,7 +716,7 @@ GatherLayout gather_layout(int64_t n_rows, int n_experts) {
 // 108, 114, 144; 16: 138, 120, 116, 143; 32: 212, 148, 121, 149; 48: 288, 186,
 // 138, 160; 64: 366, 225, 163, 162; 128: 678, 393, 255, 179.  With 8 experts
 // 32-row tiles lead up to 24: 14.7 against 23.4 and 16.1.
-constexpr int kNarrowRows = 10, kMiddleRows = 24, kManyRows = 64;
+constexpr int64_t kNarrowRows = 10, kMiddleRows = 24, kManyRows = 64;
 
 // Row tiles at most: every expert can end in a partial one, and each holds a row.
 int64_t most_tiles(int64_t n_rows, int n_experts, int tm) {
@@ -723,87 +724,79 @@ int64_t most_tiles(int64_t n_rows, int n_experts, int tm) {
   return m < n_rows ? m : n_rows;
 }
 
-hipError_t launch_product(const Mxfp4Product& g, const int32_t* offs, const int32_t* order,
-                          hipStream_t stream) {
+// Rows up to which the gather form groups them inside the product's launch.
+constexpr int kDirectRows = 64;
+constexpr int kStreamWaves = 4;    // 8 measured the same where rows are many, 2-8% slower where few
+
+// The kernel that takes a product, and its grid.
+struct Shape {
+  bool big, direct;
+  int nb;                          // stream: 16-row groups per tile
+  int col_tiles;
+  int64_t blocks;
+};
+Shape shape_of(const Mxfp4Product& g, bool gather) {
+  Shape s{};
+  const int64_t rows = g.n_rows, e = g.n_experts;
+  s.big = !gather && rows >= kManyRows * e;
+  if (s.big) {
+    const int cols = g.w_up ? 128 : 256;
+    s.col_tiles = int((g.n_dim + cols - 1) / cols);
+    s.blocks = most_tiles(rows, g.n_experts, big::kBM) * s.col_tiles;
+    s.blocks = (s.blocks + kXcds - 1) / kXcds * kXcds;
+    return s;
+  }
+  s.nb = rows < kNarrowRows * e ? 1 : (rows < kMiddleRows * e ? 2 : 4);
+  s.direct = gather && s.nb == 1 && rows <= kDirectRows;
+  const int cols = kStreamWaves * (g.w_up ? 16 : 32);
+  s.col_tiles = int((g.n_dim + cols - 1) / cols);
+  s.blocks = (most_tiles(rows, g.n_experts, 16 * s.nb) + kXcds - 1) / kXcds * kXcds * s.col_tiles;
+  return s;
+}
+
+// index: expert offsets, or with s.direct the expert of each row.
+hipError_t launch_product(const Mxfp4Product& g, const Shape& s, const int32_t* index,
+                          const int32_t* order, hipStream_t stream) {
   const uint8_t *x = static_cast<const uint8_t*>(g.rows), *w = static_cast<const uint8_t*>(g.w),
                 *u = static_cast<const uint8_t*>(g.w_up);
   uint16_t* y = static_cast<uint16_t*>(g.y);
-  if (!order && g.n_rows >= int64_t(kManyRows) * g.n_experts) {
-    const int nt = int((g.n_dim + (u ? 127 : 255)) / (u ? 128 : 256));
-    const int64_t mt = most_tiles(g.n_rows, g.n_experts, big::kBM);
-    const unsigned blocks = unsigned((mt * nt + kXcds - 1) / kXcds * kXcds);
-    auto run = [&](auto kernel) {
-      kernel<<<blocks, big::kThreads, 0, stream>>>(x, g.row_scales, int(g.n_rows), int(g.k_dim), offs, g.n_experts, w, g.w_scales, u, g.w_up_scales, int(g.n_dim), y, nt);
-    };
-    switch (((g.k_dim + 255) / 256 - 1) % 4 * 2 + (u ? 1 : 0)) {
-      case 0: run(big::tile_kernel<false, 1>); break;
-      case 1: run(big::tile_kernel<true, 1>); break;
-      case 2: run(big::tile_kernel<false, 2>); break;
-      case 3: run(big::tile_kernel<true, 2>); break;
-      case 4: run(big::tile_kernel<false, 3>); break;
-      case 5: run(big::tile_kernel<true, 3>); break;
-      case 6: run(big::tile_kernel<false, 4>); break;
-      default: run(big::tile_kernel<true, 4>); break;
-    }
-    return hipGetLastError();
-  }
-  auto run = [&](auto kernel, int tm, int waves) {
-    const int cols = waves * (u ? 16 : 32);
-    const int groups = int((g.n_dim + cols - 1) / cols);
-    const int64_t m = most_tiles(g.n_rows, g.n_experts, tm);
-    const unsigned grid = unsigned((m + kXcds - 1) / kXcds * kXcds * groups);
-    kernel<<<grid, waves * kWave, 0, stream>>>(x, g.row_scales, int(g.n_rows), int(g.k_dim), offs, g.n_experts, order, w, g.w_scales, u, g.w_up_scales, int(g.n_dim), y, groups);
+  const int n_rows = int(g.n_rows), k = int(g.k_dim), n = int(g.n_dim);
+  const unsigned blocks = unsigned(s.blocks);
+  auto big_kernel = [&](auto kernel) {
+    kernel<<<blocks, big::kThreads, 0, stream>>>(x, g.row_scales, n_rows, k, index, g.n_experts, w, g.w_scales, u, g.w_up_scales, n, y, s.col_tiles);
   };
-  const int64_t mean = g.n_rows / g.n_experts;
-  constexpr int W = 4;
-  auto pick = [&](auto glu, auto nb) {
+  auto stream_kernel = [&](auto kernel) {
+    kernel<<<blocks, kStreamWaves * kWave, 0, stream>>>(x, g.row_scales, n_rows, k, index, g.n_experts, order, w, g.w_scales, u, g.w_up_scales, n, y, s.col_tiles);
+  };
+  auto pick = [&](auto glu, auto x4) {
+    constexpr bool G = decltype(glu)::value, X4 = decltype(x4)::value;
+    constexpr int W = kStreamWaves;
+    if (s.direct) stream_kernel(stream::stream_kernel<G, 1, W, X4, true>);
+    else if (s.nb == 1) stream_kernel(stream::stream_kernel<G, 1, W, X4, false>);
+    else if (s.nb == 2) stream_kernel(stream::stream_kernel<G, 2, W, X4, false>);
+    else stream_kernel(stream::stream_kernel<G, 4, W, X4, false>);
+  };
+  auto go = [&](auto glu) {
     constexpr bool G = decltype(glu)::value;
-    constexpr int NB = decltype(nb)::value;
-    if (g.k_dim % 512 == 0) run(stream::stream_kernel<G, NB, W, true, false>, 16 * NB, W);
-    else run(stream::stream_kernel<G, NB, W, false, false>, 16 * NB, W);
+    if (s.big) {
+      switch ((k + 255) / 256 % 4) {
+        case 1: return big_kernel(big::tile_kernel<G, 1>);
+        case 2: return big_kernel(big::tile_kernel<G, 2>);
+        case 3: return big_kernel(big::tile_kernel<G, 3>);
+        default: return big_kernel(big::tile_kernel<G, 4>);
+      }
+    }
+    if (k % 512 == 0) pick(glu, std::true_type());
+    else pick(glu, std::false_type());
   };
-  auto by_rows = [&](auto glu) {
-    if (mean < kNarrowRows) pick(glu, std::integral_constant<int, 1>());
-    else if (mean < kMiddleRows) pick(glu, std::integral_constant<int, 2>());
-    else pick(glu, std::integral_constant<int, 4>());
-  };
-  if (u) by_rows(std::true_type());
-  else by_rows(std::false_type());
-  return hipGetLastError();
-}
-
-// Rows up to which the gather form groups them inside the product's launch.
-constexpr int kDirectRows = 64;
-
-hipError_t launch_direct(const Mxfp4Product& g, const int32_t* row_expert, hipStream_t stream) {
-  constexpr int W = 4;
-  const int cols = W * (g.w_up ? 16 : 32);
-  const int groups = int((g.n_dim + cols - 1) / cols);
-  const int64_t m = most_tiles(g.n_rows, g.n_experts, 16);
-  const unsigned grid = unsigned((m + kXcds - 1) / kXcds * kXcds * groups);
-  auto run = [&](auto kernel) {
-    kernel<<<grid, W * kWave, 0, stream>>>(
-        static_cast<const uint8_t*>(g.rows), g.row_scales, int(g.n_rows), int(g.k_dim), row_expert,
-        g.n_experts, nullptr, static_cast<const uint8_t*>(g.w), g.w_scales,
-        static_cast<const uint8_t*>(g.w_up), g.w_up_scales, int(g.n_dim),
-        static_cast<uint16_t*>(g.y), groups);
-  };
-  const bool x4 = g.k_dim % 512 == 0;
-  if (g.w_up) {
-    if (x4) run(stream::stream_kernel<true, 1, W, true, true>);
-    else run(stream::stream_kernel<true, 1, W, false, true>);
-  } else {
-    if (x4) run(stream::stream_kernel<false, 1, W, true, true>);
-    else run(stream::stream_kernel<false, 1, W, false, true>);
-  }
+  if (u) go(std::true_type());
+  else go(std::false_type());
   return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t gemm_mxfp4_tiles(int64_t n_rows, int n_experts, int64_t n_dim) {
-  return ((n_rows + 15) / 16 + n_experts + kXcds) * ((n_dim + 127) / 128);
-}
+int64_t gemm_mxfp4_blocks(const Mxfp4Product& g, bool gather) { return shape_of(g, gather).blocks; }
 
 size_t gather_gemm_mxfp4_workspace_bytes(int64_t n_rows, int n_experts) {
   return gather_layout(n_rows, n_experts).total;
@@ -811,13 +804,13 @@ size_t gather_gemm_mxfp4_workspace_bytes(int64_t n_rows, int n_experts) {
 
 hipError_t launch_grouped_gemm_mxfp4(const Mxfp4Product& g, const int32_t* expert_offsets,
                                      hipStream_t stream) {
-  return launch_product(g, expert_offsets, nullptr, stream);
+  return launch_product(g, shape_of(g, false), expert_offsets, nullptr, stream);
 }
 
 hipError_t launch_gather_gemm_mxfp4(const Mxfp4Product& g, const int32_t* row_expert,
                                     void* workspace, hipStream_t stream) {
-  if (g.n_rows <= kDirectRows && g.n_rows < int64_t(kNarrowRows) * g.n_experts)
-    return launch_direct(g, row_expert, stream);
+  const Shape s = shape_of(g, true);
+  if (s.direct) return launch_product(g, s, row_expert, nullptr, stream);
   const GatherLayout L = gather_layout(g.n_rows, g.n_experts);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   DispatchArgs d{};
@@ -835,7 +828,7 @@ hipError_t launch_gather_gemm_mxfp4(const Mxfp4Product& g, const int32_t* row_ex
   d.workspace = ws + L.dispatch_ws;
   const hipError_t err = launch_dispatch(d, stream);
   if (err != hipSuccess) return err;
-  return launch_product(g, d.expert_offsets, d.src_pair, stream);
+  return launch_product(g, s, d.expert_offsets, d.src_pair, stream);
 }
 
 }  // namespace moe

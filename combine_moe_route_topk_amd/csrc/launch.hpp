@@ -13,6 +13,13 @@ namespace moe {
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 64;
 
+// A launch holds fewer than 2^32 threads in x: 2^22 workgroups of at most 1024
+// threads there, the rest in y (block_id() of device_common.hpp counts them).
+inline dim3 grid_of(int64_t blocks) {
+  const int64_t x = blocks < (int64_t(1) << 22) ? blocks : int64_t(1) << 22;
+  return dim3(unsigned(x), unsigned((blocks + x - 1) / x));
+}
+
 hipError_t launch_route_topk(const float* logits, int64_t n_tokens, int n_experts, int k,
                              int renormalize, int32_t* topk_idx, float* topk_w,
                              hipStream_t stream);
@@ -163,8 +170,10 @@ struct Mxfp4Product {
   int64_t n_dim;
   void* y;
 };
-// Worst-case workgroup count, for the caller's int32 range check.
-int64_t gemm_mxfp4_tiles(int64_t n_rows, int n_experts, int64_t n_dim);
+// Workgroups of the product's launch (gather: rows in any order), of which one
+// launch takes kMaxMxfp4Blocks (256 threads each).
+constexpr int64_t kMaxMxfp4Blocks = (int64_t(1) << 24) - 1;
+int64_t gemm_mxfp4_blocks(const Mxfp4Product& g, bool gather);
 hipError_t launch_grouped_gemm_mxfp4(const Mxfp4Product& g, const int32_t* expert_offsets,
                                      hipStream_t stream);
 size_t gather_gemm_mxfp4_workspace_bytes(int64_t n_rows, int n_experts);

@@ -67,7 +67,7 @@ template <typename T>
 __global__ __launch_bounds__(kBlock) void quantize_kernel(const T* __restrict__ x, int64_t n_groups,
                                                           uint32_t* __restrict__ codes,
                                                           uint8_t* __restrict__ scales) {
-  const int64_t g0 = int64_t(blockIdx.x) * (kBlock * kU) + threadIdx.x;
+  const int64_t g0 = block_id() * (kBlock * kU) + threadIdx.x;
   float v[kU][8];
 #pragma unroll
   for (int u = 0; u < kU; ++u) {
@@ -108,7 +108,7 @@ template <typename T>
 __global__ __launch_bounds__(kBlock) void dequant_kernel(const uint32_t* __restrict__ codes,
                                                          const uint8_t* __restrict__ scales,
                                                          int64_t n_groups, T* __restrict__ out) {
-  const int64_t g0 = int64_t(blockIdx.x) * (kBlock * kU) + threadIdx.x;
+  const int64_t g0 = block_id() * (kBlock * kU) + threadIdx.x;
   uint32_t q[kU];
   int byte[kU];
 #pragma unroll
@@ -139,7 +139,7 @@ __global__ __launch_bounds__(kBlock) void dequant_kernel(const uint32_t* __restr
 hipError_t launch_quantize_mxfp4(const void* x, int x_bf16, int64_t n_elems, void* codes,
                                  uint8_t* scales, hipStream_t stream) {
   const int64_t groups = n_elems / 8;
-  const unsigned blocks = unsigned((groups + kBlock * kU - 1) / (kBlock * kU));
+  const dim3 blocks = grid_of((groups + kBlock * kU - 1) / (kBlock * kU));
   if (x_bf16)
     quantize_kernel<uint16_t><<<blocks, kBlock, 0, stream>>>(static_cast<const uint16_t*>(x), groups,
                                                              static_cast<uint32_t*>(codes), scales);
@@ -152,7 +152,7 @@ hipError_t launch_quantize_mxfp4(const void* x, int x_bf16, int64_t n_elems, voi
 hipError_t launch_dequant_mxfp4(const void* codes, const uint8_t* scales, int64_t n_elems, void* out,
                                 int out_bf16, hipStream_t stream) {
   const int64_t groups = n_elems / 8;
-  const unsigned blocks = unsigned((groups + kBlock * kU - 1) / (kBlock * kU));
+  const dim3 blocks = grid_of((groups + kBlock * kU - 1) / (kBlock * kU));
   if (out_bf16)
     dequant_kernel<uint16_t><<<blocks, kBlock, 0, stream>>>(static_cast<const uint32_t*>(codes), scales,
                                                             groups, static_cast<uint16_t*>(out));

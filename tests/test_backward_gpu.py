@@ -280,3 +280,21 @@ def test_rows_past_four_gibibytes():
     assert bool((d_y[-2:] == 1.5).all()) and bool((d_y[:4] == 0).all())
     x = moe.moe_dispatch_backward(d_y, pos, k)
     assert bool((x[-1] == 3.0).all()) and bool((x[:2] == 0).all())
+
+
+def test_more_pairs_than_one_launch_has_threads():
+    """70 million pairs: a wave each is more than 2^32 threads."""
+    n = 70_000_000
+    pos = torch.arange(n - 1, -1, -1, dtype=torch.int32, device=DEV)
+    g = torch.arange(n, device=DEV, dtype=torch.int32).remainder_(1000).float().unsqueeze(1)
+    w = torch.full((n, 1), 0.5, device=DEV)
+    d_y, d_w = moe.moe_combine_backward(g, torch.full((n, 1), 2.0, device=DEV), pos, w)
+    assert torch.equal(d_w, 2 * g) and torch.equal(d_y.flip(0), 0.5 * g)
+    del d_w
+    x = moe.moe_dispatch_backward(d_y, pos, 1)
+    assert torch.equal(x, 0.5 * g)
+    assert torch.equal(moe.moe_combine(d_y, pos, w), 0.25 * g)        # the forward call, too
+    del x, d_y
+    idx = torch.zeros((n, 1), dtype=torch.int32, device=DEV)
+    d = moe.moe_route_topk_backward(idx, w, g, 1)
+    assert torch.equal(d, 0.5 * (g - 0.5 * g))

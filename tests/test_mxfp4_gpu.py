@@ -278,6 +278,28 @@ def test_products_of_many_rows(k, glu):
         _check(to_np(_run("grouped", rows, rs, ids, w, up)), rows, rs, ids, w, up, f"K={k}")
 
 
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("r,e,k,n", [(64, 7, 512, 70), (64, 64, 128, 36), (64, 1024, 256, 20), (17, 2, 640, 129),
+                                     (64, 40, 1152, 8), (65, 7, 512, 70)])
+def test_gather_of_a_small_batch(r, e, k, n, glu):
+    """Up to 64 rows are grouped inside the product's launch: repeated experts
+    past a tile of 16, ids outside the range between them, all rows one expert."""
+    rng = np.random.default_rng(r + e)
+    rows, rs = _operand(rng, r, k)
+    w, up = _operand(rng, e, n, k), _operand(rng, e, n, k) if glu else None
+    if glu:
+        rs, w = (rs - np.uint8(4)).astype(np.uint8), (w[0], (w[1] - np.uint8(3)).astype(np.uint8))
+    for ids in (rng.integers(0, e, r), np.full(r, e - 1), np.where(np.arange(r) % 3, e - 1, rng.integers(-2, e + 2, r)),
+                np.sort(rng.integers(0, e, r))[::-1]):
+        ids = ids.astype(np.int32)
+        y = torch.full((r, n), 7.0, dtype=torch.bfloat16, device=DEV)
+        _run("gather", rows, rs, ids, w, up, y=y)
+        good = (ids >= 0) & (ids < e)
+        assert (as_f32(to_np(y))[~good] == 7).all()
+        with np.errstate(over="ignore"):
+            _check(to_np(y)[good], rows[good], rs[good], ids[good], w, up, f"R={r} E={e} glu={glu}")
+
+
 def test_weights_past_four_gibibytes():
     """Weight and output offsets beyond 2^32 bytes: the last expert of 4.6 GB."""
     e, n, k = 9, 65536, 16384
@@ -367,15 +389,17 @@ def test_expert_layer_as_it_is_used(n, e, k, d, f, gather):
     assert tuple(out.shape) == (n, d) and bool(torch.isfinite(out.float()).all())
 
 
-def test_products_on_another_stream_and_in_a_graph():
+@pytest.mark.parametrize("r,offs", [(90, [0, 10, 10, 40, 41, 75, 90]), (40, [0, 10, 10, 20, 21, 35, 40]),
+                                    (600, [0, 100, 100, 300, 301, 555, 600])])
+def test_products_on_another_stream_and_in_a_graph(r, offs):
     """Two captured layers that share a workspace replay one after the other;
     every replay equals the eager result bit for bit."""
     rng = np.random.default_rng(9)
-    r, e, k, n = 90, 6, 384, 200
+    e, k, n = 6, 384, 200
     x = to_dev(rng.standard_normal((r, k)).astype(np.float32))
     w, up = ([to_dev(t) for t in _operand(rng, e, n, k)] for _ in range(2))
     ids = to_dev(rng.integers(0, e, r).astype(np.int32))
-    offs = to_dev(np.array([0, 10, 10, 40, 41, 75, 90], np.int32))
+    offs = to_dev(np.array(offs, np.int32))
     ws = torch.empty(moe.moe_gather_gemm_mxfp4_workspace_bytes(r, e), dtype=torch.uint8, device=DEV)
     c, s = torch.empty((r, k // 2), dtype=torch.uint8, device=DEV), torch.empty((r, k // 32), dtype=torch.uint8, device=DEV)
     outs = [torch.empty((r, n), dtype=torch.bfloat16, device=DEV) for _ in range(3)]
