@@ -339,8 +339,10 @@ int moe_dispatch_backward(const void* d_rows, int32_t rows_dtype, int64_t n_toke
  *   logits    [N, E] float32;  topk_idx, topk_w [N, k] from moe_route_topk with
  *             the same renormalize (slot 0 the largest logit)
  *   d_topk_w  [N, k] float32;  d_logits [N, E] float32, output (every element)
- * Slots whose id lies outside [0, E) add nothing.  A row whose logits are all
- * -inf has NaN weights in the forward call and a NaN gradient here.
+ * Slots whose id lies outside [0, E) add nothing.  A logit of -inf has
+ * probability 0.  NaN among a row's weights (moe_route_topk writes them where
+ * a -inf logit enters a weight) makes the gradient of its selected experts
+ * (renormalize == 0: of all) NaN.
  * Errors: those of moe_route_topk. */
 int moe_route_topk_backward(const float* logits, const int32_t* topk_idx, const float* topk_w,
                             const float* d_topk_w, int64_t n_tokens, int32_t n_experts, int32_t k,

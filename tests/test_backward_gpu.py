@@ -162,6 +162,28 @@ def test_route_backward_skips_bad_ids_and_adds_repeated_ones():
     assert got.tolist() == [[0.5, 0, -0.5, 0], [0, 0.25, 0, 0]]
 
 
+@pytest.mark.parametrize("renorm", [True, False])
+def test_rows_of_masked_experts(renorm):
+    """Fewer experts left than slots: the masked slots weigh 0 and get gradient 0.
+    Weights of NaN (a row with every expert masked) give NaN where they reach."""
+    n, e, k = 5, 70, 4
+    rng = np.random.default_rng(4)
+    l = rng.standard_normal((n, e)).astype(np.float32)
+    l[1, 2:] = -np.inf                          # two experts for four slots
+    l[2, 1:] = -np.inf
+    l[4, 3:] = np.finfo(np.float32).min
+    idx, w = route_topk(l, k, renorm)
+    l[3], w[3] = -np.inf, np.nan
+    d = rng.standard_normal((n, k)).astype(np.float32)
+    got = to_np(moe.moe_route_topk_backward(to_dev(idx), to_dev(w), to_dev(d), e, renorm, to_dev(l)))
+    ok = [0, 1, 2, 4]
+    want, scale = route_backward(idx[ok], w[ok], d[ok], e, renorm, l[ok])
+    gap = 0.0 if renorm else np.where(np.isfinite(l[ok]), l[ok].max(1, keepdims=True) - l[ok], 104.0).clip(0, 104.0) + 22
+    assert (np.abs(got[ok] - want) <= (k + 4 + gap) * U * scale + 2.0 ** -126).all()
+    assert (got[1, 2:] == 0).all() and (got[2, 1:] == 0).all()
+    assert np.isnan(got[3][idx[3]]).all()
+
+
 def test_gradient_of_a_run_matches_autograd():
     """Route, dispatch, identity experts with a per-row gain, combine and back:
     the three gradients chained against torch's autograd in float64."""

@@ -192,10 +192,11 @@ def test_products_exact_where_sums_are(kind, r, e, k, n):
 
 
 @pytest.mark.parametrize("kind", ["grouped", "gather"])
-def test_each_block_takes_its_own_scales(kind):
-    """One block of one row and one column at a time is scaled by 2^10: the
-    output moves by that block's share alone."""
-    k, r, n, e = 1408, 40, 48, 2
+@pytest.mark.parametrize("r,k", [(40, 1408), (40, 1536), (300, 1408), (300, 1536), (300, 2048)])
+def test_each_block_takes_its_own_scales(kind, r, k):
+    """Every block's scale is raised in one row and in one column, by 2^3 and 2^4:
+    the outputs move by those blocks' shares alone."""
+    n, e = 48, 2
     rows = np.full((r, k // 2), 0x22, np.uint8)                      # ones
     w = np.full((e, n, k // 2), 0x22, np.uint8)
     rs, ws = np.full((r, k // 32), 127, np.uint8), np.full((e, n, k // 32), 127, np.uint8)
@@ -209,10 +210,11 @@ def test_each_block_takes_its_own_scales(kind):
 
 
 @pytest.mark.parametrize("kind", ["grouped", "gather"])
-def test_extreme_scales_and_nan_scales(kind):
+@pytest.mark.parametrize("r,k", [(6, 256), (200, 256), (200, 384), (70, 1024), (200, 1024)])
+def test_extreme_scales_and_nan_scales(kind, r, k):
     """Scale bytes 0 and 254 (their product is finite again); 255 makes a row or
     a column NaN and leaves the others."""
-    r, e, k, n = 6, 1, 256, 40
+    e, n = 1, 40
     rows, w = np.full((r, k // 2), 0x22, np.uint8), np.full((e, n, k // 2), 0x22, np.uint8)
     rs, ws = np.full((r, k // 32), 0, np.uint8), np.full((e, n, k // 32), 254, np.uint8)
     rs[1, 3], ws[0, 7, 2] = 255, 255
