@@ -23,40 +23,49 @@ namespace {
 
 constexpr int kBlock = 256;
 // Groups of 8 per thread.  Measured on 16384 x 14336 bf16, quantising: 1, 2, 4
-// and 8 groups 98, 96, 107 and 106 us (2 is 6.2 TB/s, also best at 4096 x 7168);
-// back to bf16: 113, 105, 100 and 106 us (5.9 TB/s).  Non-temporal loads gain 6%
-// there and lose 17% at 4096 x 7168, where the last-level cache holds x.
+// and 8 groups 98, 96, 107 and 106 us (2 also best at 4096 x 7168); back to
+// bf16, with ordinary stores: 113, 105, 100 and 106 us.
 constexpr int kQuant = 2, kDequant = 4;
+
+// bf16 x beyond the last-level cache (256 MB) is loaded past it: 98 -> 90 us at
+// 470 MB (6.6 TB/s); at 59 MB, which the cache holds, that costs 17% (11.9 ->
+// 13.9).  fp32 x of 940 MB takes 190 us either way.
+constexpr int64_t kCacheBytes = int64_t(256) << 20;
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // 8 consecutive elements as fp32.
+template <bool NT>
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   const u32x4 a = *reinterpret_cast<const u32x4*>(p);
   const u32x4 b = *reinterpret_cast<const u32x4*>(p + 4);
 #pragma unroll
   for (int i = 0; i < 4; ++i) { v[i] = __uint_as_float(a[i]); v[4 + i] = __uint_as_float(b[i]); }
 }
+template <bool NT>
 __device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
-  const u32x4 a = *reinterpret_cast<const u32x4*>(p);
+  const u32x4* q = reinterpret_cast<const u32x4*>(p);
+  const u32x4 a = NT ? __builtin_nontemporal_load(q) : *q;
 #pragma unroll
   for (int i = 0; i < 4; ++i) unpack_bf16x2(a[i], v[2 * i], v[2 * i + 1]);
 }
+// Values are stored past the caches: 100 -> 84 us for 16384 x 14336 bf16 (7.1
+// TB/s), 11.9 -> 9.9 for 4096 x 7168.
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   u32x4 a, b;
 #pragma unroll
   for (int i = 0; i < 4; ++i) { a[i] = __float_as_uint(v[i]); b[i] = __float_as_uint(v[4 + i]); }
-  *reinterpret_cast<u32x4*>(p) = a;
-  *reinterpret_cast<u32x4*>(p + 4) = b;
+  __builtin_nontemporal_store(a, reinterpret_cast<u32x4*>(p));
+  __builtin_nontemporal_store(b, reinterpret_cast<u32x4*>(p + 4));
 }
 __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
   u32x4 a;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     a[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[2 * i], v[2 * i + 1]}, bf16x2));
-  *reinterpret_cast<u32x4*>(p) = a;
+  __builtin_nontemporal_store(a, reinterpret_cast<u32x4*>(p));
 }
 
 // Maximum over the four lanes of a quad (DPP quad permutes).
@@ -67,7 +76,7 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
   return o > v ? o : v;
 }
 
-template <typename T>
+template <typename T, bool NT>
 __global__ __launch_bounds__(kBlock) void quantize_kernel(const T* __restrict__ x, int64_t n_groups,
                                                           uint32_t* __restrict__ codes,
                                                           uint8_t* __restrict__ scales) {
@@ -76,7 +85,7 @@ __global__ __launch_bounds__(kBlock) void quantize_kernel(const T* __restrict__ 
 #pragma unroll
   for (int u = 0; u < kQuant; ++u) {
     const int64_t g = g0 + u * kBlock;
-    if (g < n_groups) load8(x + g * 8, v[u]);   // quads are whole: n_groups is a multiple of 4
+    if (g < n_groups) load8<NT>(x + g * 8, v[u]);   // quads are whole: n_groups is a multiple of 4
   }
 #pragma unroll
   for (int u = 0; u < kQuant; ++u) {
@@ -144,12 +153,15 @@ hipError_t launch_quantize_mxfp4(const void* x, int x_bf16, int64_t n_elems, voi
                                  uint8_t* scales, hipStream_t stream) {
   const int64_t groups = n_elems / 8;
   const dim3 blocks = grid_of((groups + kBlock * kQuant - 1) / (kBlock * kQuant));
-  if (x_bf16)
-    quantize_kernel<uint16_t><<<blocks, kBlock, 0, stream>>>(static_cast<const uint16_t*>(x), groups,
-                                                             static_cast<uint32_t*>(codes), scales);
+  auto run = [&](auto kernel, auto* p) {
+    kernel<<<blocks, kBlock, 0, stream>>>(p, groups, static_cast<uint32_t*>(codes), scales);
+  };
+  if (!x_bf16)
+    run(quantize_kernel<float, false>, static_cast<const float*>(x));
+  else if (n_elems * 2 > kCacheBytes)
+    run(quantize_kernel<uint16_t, true>, static_cast<const uint16_t*>(x));
   else
-    quantize_kernel<float><<<blocks, kBlock, 0, stream>>>(static_cast<const float*>(x), groups,
-                                                          static_cast<uint32_t*>(codes), scales);
+    run(quantize_kernel<uint16_t, false>, static_cast<const uint16_t*>(x));
   return hipGetLastError();
 }
 

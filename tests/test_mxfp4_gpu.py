@@ -56,6 +56,22 @@ def test_quantize_normal(dtype, r, k):
     _same_quantize(x, dtype)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_quantize_beyond_the_cache(dtype):
+    """More than 256 MB of x are loaded another way: the same codes as of its parts."""
+    r, k = (4100, 32768) if dtype == torch.bfloat16 else (4100, 16416)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    x = torch.randn((r, k), generator=g, device=DEV).to(dtype)
+    c, s = moe.moe_quantize_mxfp4(x)
+    for lo, hi in ((0, 2000), (2000, 4100)):
+        pc, ps = moe.moe_quantize_mxfp4(x[lo:hi])
+        assert torch.equal(c[lo:hi], pc) and torch.equal(s[lo:hi], ps)
+    rows = [0, 1999, 4099]
+    wc, ws = quantize(x[rows].float().cpu().numpy())
+    assert np.array_equal(to_np(c[rows]), wc) and np.array_equal(to_np(s[rows]), ws)
+
+
 def test_quantize_every_bf16_pattern():
     """Each finite bf16 value as the largest of a block with random smaller
     ones, and within a block of a random larger one."""
