@@ -40,9 +40,10 @@ def _stream(stream) -> ctypes.c_void_p:
 
 def _launch(fn: str, dev: torch.device, stream, args, own=()) -> None:
     """Call C function `fn` with its stream on the operands' device, whichever
-    device and stream are current.  `own`: tensors allocated in the call; on
-    another stream than the current one their memory must not be handed out
-    again before that stream has passed the call."""
+    device and stream are current.  `own`: tensors allocated in the call.
+    Their memory belongs to the current stream: another one waits for what
+    still uses it there, and it is not handed out again before that stream has
+    passed the call."""
     # the raw handle: torch.cuda.current_stream() takes 2 us to build its object
     cur = torch._C._cuda_getCurrentRawStream(dev.index)
     if stream is None:
@@ -51,6 +52,8 @@ def _launch(fn: str, dev: torch.device, stream, args, own=()) -> None:
         raise ValueError(f"{fn}: the stream is on {stream.device}, the operands on {dev}")
     else:
         raw = stream.cuda_stream
+        if raw != cur and own:
+            stream.wait_stream(torch.cuda.current_stream(dev))
     if dev.index == torch.cuda.current_device():
         check(fn, getattr(lib, fn)(*args, raw))
     else:

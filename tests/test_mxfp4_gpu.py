@@ -453,3 +453,23 @@ def test_products_on_another_stream_and_in_a_graph(r, offs):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(kept, eager))
         step()
+
+
+def test_memory_still_in_use_on_the_current_stream():
+    """An output allocated by a call on another stream may get memory that a
+    freed tensor's kernels, queued on the current stream, still write."""
+    r, k = 4096, 4096
+    x = torch.randn((r, k), device=DEV)
+    want = [t.clone() for t in moe.moe_quantize_mxfp4(x)]
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        old = [torch.empty((r, k // 2), dtype=torch.uint8, device=DEV), torch.empty((r, k // 32), dtype=torch.uint8, device=DEV)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        for t in old:
+            t.fill_(9)
+        del t, old
+        got = moe.moe_quantize_mxfp4(x, stream=side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        del got
