@@ -27,31 +27,52 @@ struct Tile {
   bool valid;
 };
 
-// m-tile index -> expert and row range.  Lane j of each 64-expert chunk counts
-// the tiles of expert c + j; a wave prefix sum finds the owner.  Row ranges are
-// clamped into [0, n_rows], so no row outside the buffer is read whatever the
-// offsets hold.
+// Row ranges of experts 4 l .. 4 l + 3 past e0 in lane l, clamped into
+// [0, n_rows], so no row outside the buffer is read whatever the offsets hold,
+// and the tiles they take.
+template <int TM>
+struct Experts {
+  static constexpr int kPer = 4;
+  int lo[kPer], hi[kPer], nt[kPer], sum;
+  __device__ Experts(int e0, const int32_t* __restrict__ offs, int n_experts, int n_rows) {
+    int at[kPer + 1];
+#pragma unroll
+    for (int i = 0; i <= kPer; ++i) {
+      const int e = e0 + kPer * lane_id() + i;
+      at[i] = offs[e < n_experts ? e : n_experts];             // past the last: no rows
+    }
+    sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int a = at[i], b = at[i + 1];
+      lo[i] = a < 0 ? 0 : (a > n_rows ? n_rows : a);
+      hi[i] = b < lo[i] ? lo[i] : (b > n_rows ? n_rows : b);
+      nt[i] = (hi[i] - lo[i]) / TM + ((hi[i] - lo[i]) % TM != 0);
+      sum += nt[i];
+    }
+  }
+};
+
+// m-tile index -> expert and row range: a wave prefix sum over each 256 experts
+// finds the lane, and the lane the expert.
 template <int TM>
 __device__ Tile find_tile(int m_idx, const int32_t* __restrict__ offs, int n_experts, int n_rows) {
   Tile t{};
-  const int lane = lane_id();
+  using X = Experts<TM>;
   int base = 0;
-  for (int c = 0; c < n_experts; c += kWave) {
-    const int e = c + lane;
-    int lo = 0, hi = 0, nt = 0;
-    if (e < n_experts) {
-      const int a = offs[e], b = offs[e + 1];
-      lo = a < 0 ? 0 : (a > n_rows ? n_rows : a);
-      hi = b < lo ? lo : (b > n_rows ? n_rows : b);
-      nt = (hi - lo) / TM + ((hi - lo) % TM != 0);
-    }
-    const int incl = wave_inclusive_scan(nt);
-    const int excl = incl - nt;
-    const uint64_t own = ballot(nt > 0 && m_idx >= base + excl && m_idx < base + incl);
+  for (int c = 0; c < n_experts; c += X::kPer * kWave) {
+    const X x(c, offs, n_experts, n_rows);
+    const int incl = wave_inclusive_scan(x.sum);
+    int at = m_idx - (base + incl - x.sum);                    // tile number within the lane's four
+    const uint64_t own = ballot(at >= 0 && at < x.sum);
     if (own) {
       const int src = __ffsll((unsigned long long)own) - 1;
-      t.expert = __builtin_amdgcn_readfirstlane(c + src);
-      t.row0 = lane_value(lo, src) + (m_idx - base - lane_value(excl, src)) * TM;
+      int i = 0, lo = x.lo[0], hi = x.hi[0];
+#pragma unroll
+      for (int j = 0; j + 1 < X::kPer; ++j)
+        if (i == j && at >= x.nt[j]) { at -= x.nt[j]; i = j + 1; lo = x.lo[j + 1]; hi = x.hi[j + 1]; }
+      t.expert = __builtin_amdgcn_readfirstlane(c + X::kPer * src + lane_value(i, src));
+      t.row0 = lane_value(lo, src) + lane_value(at, src) * TM;
       t.row_end = lane_value(hi, src);
       t.valid = true;
       return t;
@@ -547,19 +568,9 @@ __device__ __forceinline__ void stage(f32x16 (&acc)[kT][kT], Frag& f0, Frag& f1,
 
 // Real row tiles of all experts, under find_tile's clamping.
 __device__ int count_tiles(const int32_t* __restrict__ offs, int n_experts, int n_rows) {
-  const int lane = lane_id();
   int total = 0;
-  for (int c = 0; c < n_experts; c += kWave) {
-    const int e = c + lane;
-    int nt = 0;
-    if (e < n_experts) {
-      const int a = offs[e], b = offs[e + 1];
-      const int lo = a < 0 ? 0 : (a > n_rows ? n_rows : a);
-      const int hi = b < lo ? lo : (b > n_rows ? n_rows : b);
-      nt = (hi - lo) / kBM + ((hi - lo) % kBM != 0);
-    }
-    total += lane_value(wave_inclusive_scan(nt), kWave - 1);
-  }
+  for (int c = 0; c < n_experts; c += Experts<kBM>::kPer * kWave)
+    total += lane_value(wave_inclusive_scan(Experts<kBM>(c, offs, n_experts, n_rows).sum), kWave - 1);
   return __builtin_amdgcn_readfirstlane(total);
 }
 
