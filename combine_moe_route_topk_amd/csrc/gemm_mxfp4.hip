@@ -395,8 +395,9 @@ constexpr int kBM = 256, kBN = 256;
 constexpr int kRowBytes = 128;                 // 256 codes
 constexpr int kTileBytes = kBM * kRowBytes;    // 32 KB per operand and stage
 constexpr int kSlotBytes = 2 * kTileBytes;
-constexpr int kLd = kTileBytes / (kThreads * 16);   // direct loads per lane, operand and stage (8)
-constexpr int kT = 4;                          // 32-row MFMA tiles of a wave, each way
+constexpr int kLd = kTileBytes / (kThreads * 16);   // direct loads per lane and stage for the columns (8)
+constexpr int kT = 4;                          // 32-column MFMA tiles of a wave; MT of 32 rows: 4, or 2
+                                               // for a tile of at most 128 rows
 constexpr int kGroupM = 8;                     // row tiles per group of the tile order
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
@@ -418,39 +419,42 @@ struct Src {
   int n_stages;
 };
 
-template <bool GLU, int LO, int HI>   // runs 0..7: rows, 8..15: columns
+template <bool GLU, int MT, int LO, int HI>   // runs 0 .. 2 MT - 1: rows, the kLd after: columns
 __device__ __forceinline__ void load_runs(unsigned char* slot, const Src& s, int wave, int d) {
+  constexpr int kRows = 2 * MT;
   const bool last = d >= s.n_stages - 1;        // stages past the end repeat the last one
   const int64_t k = int64_t(last ? s.n_stages - 1 : d) * kRowBytes;
   const uint32_t back = last ? s.back : 0u;
 #pragma unroll
   for (int i = LO; i < HI; ++i) {
-    const int run = ((i % kLd) * 4 + wave) * 1024;
-    const uint8_t* base = (i < kLd ? s.base[0] : s.base[GLU && i % kLd >= kLd / 2 ? 2 : 1]) + k;
-    const uint32_t o = (i < kLd ? s.a_off[i] : s.b_off[i - kLd]) - back;
-    __builtin_amdgcn_global_load_lds(base + o, (lds_ptr)(slot + (i < kLd ? 0 : kTileBytes) + run), 16, 0, 0);
+    const int run = ((i < kRows ? i : i - kRows) * 4 + wave) * 1024;
+    const uint8_t* base = (i < kRows ? s.base[0] : s.base[GLU && i - kRows >= kLd / 2 ? 2 : 1]) + k;
+    const uint32_t o = (i < kRows ? s.a_off[i] : s.b_off[i - kRows]) - back;
+    __builtin_amdgcn_global_load_lds(base + o, (lds_ptr)(slot + (i < kRows ? 0 : kTileBytes) + run), 16, 0, 0);
   }
 }
 
+template <int MT>
 struct Frag {
-  i32x4 a[kT], b[kT];
+  i32x4 a[MT], b[kT];
 };
 struct Lds {
   int a_row, b_row[kT], chunk[4];
 };
-__device__ __forceinline__ void read_frag(const unsigned char* slot, const Lds& l, int kk, Frag& f) {
+template <int MT>
+__device__ __forceinline__ void read_frag(const unsigned char* slot, const Lds& l, int kk, Frag<MT>& f) {
 #pragma unroll
-  for (int i = 0; i < kT; ++i)
+  for (int i = 0; i < MT; ++i)
     f.a[i] = *reinterpret_cast<const i32x4*>(slot + l.a_row + i * 32 * kRowBytes + l.chunk[kk]);
 #pragma unroll
   for (int j = 0; j < kT; ++j)
     f.b[j] = *reinterpret_cast<const i32x4*>(slot + kTileBytes + l.b_row[j] + l.chunk[kk]);
 }
 
-template <int KK>
-__device__ __forceinline__ void mma(f32x16 (&acc)[kT][kT], const Frag& f, const int (&sa)[kT], const int (&sb)[kT]) {
+template <int KK, int MT>
+__device__ __forceinline__ void mma(f32x16 (&acc)[MT][kT], const Frag<MT>& f, const int (&sa)[MT], const int (&sb)[kT]) {
 #pragma unroll
-  for (int i = 0; i < kT; ++i)
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < kT; ++j) {
       const i32x8 a = {f.a[i].x, f.a[i].y, f.a[i].z, f.a[i].w, 0, 0, 0, 0};
@@ -459,35 +463,38 @@ __device__ __forceinline__ void mma(f32x16 (&acc)[kT][kT], const Frag& f, const 
     }
 }
 
-// Issue order of one slice: 16 MFMAs, the first R each followed by an LDS
+// Issue order of one slice: its 4 MT MFMAs, the first R each followed by an LDS
 // read, N direct loads spread between them.
-template <int R, int N>
+template <int MT, int R, int N>
 __device__ __forceinline__ void slice_order() {
+  constexpr int kM = MT * kT;
+  static_assert(R <= kM && N <= kM, "at most one of each per MFMA");
 #pragma unroll
-  for (int q = 0; q < 16; ++q) {
+  for (int q = 0; q < kM; ++q) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                     // MFMA
     if (q < R) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);          // LDS read
-    if ((q * N) / 16 != ((q + 1) * N) / 16) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    if ((q * N) / kM != ((q + 1) * N) / kM) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
   }
 }
 
-// Scale dwords of four stages for 8 rows (4 of each operand): [stage][row].
+// Scale dwords of four stages for MT rows and kT columns: [stage][row].
+template <int MT>
 struct Scales {
-  int a[4][kT], b[4][kT];
+  int a[4][MT], b[4][kT];
 };
 struct ScaleSrc {
   const uint8_t* base[3];
   uint32_t a_off[kT], b_off[kT];
   int n_bytes;                     // K / 32
 };
-template <bool GLU, bool FULL>       // FULL: the four stages are all within K
-__device__ __forceinline__ void load_scales(const ScaleSrc& s, int super, int half, int (&raw)[2 * kT][4]) {
+template <bool GLU, bool FULL, int MT>   // FULL: the four stages are all within K
+__device__ __forceinline__ void load_scales(const ScaleSrc& s, int super, int half, int (&raw)[MT + kT][4]) {
   const uint32_t first = 32 * super + 16 * half;
   if (FULL || 32 * super + 32 <= s.n_bytes) {
 #pragma unroll
-    for (int i = 0; i < 2 * kT; ++i) {
-      const uint8_t* base = s.base[i < kT ? 0 : (GLU && i % kT >= 2 ? 2 : 1)];
-      const u32x4a q = *reinterpret_cast<const u32x4a*>(base + ((i < kT ? s.a_off[i % kT] : s.b_off[i % kT]) + first));
+    for (int i = 0; i < MT + kT; ++i) {
+      const uint8_t* base = s.base[i < MT ? 0 : (GLU && i - MT >= 2 ? 2 : 1)];
+      const u32x4a q = *reinterpret_cast<const u32x4a*>(base + ((i < MT ? s.a_off[i] : s.b_off[i - MT]) + first));
       raw[i][0] = q.x; raw[i][1] = q.y; raw[i][2] = q.z; raw[i][3] = q.w;
     }
   } else {                                       // K ends in these four stages
@@ -496,26 +503,24 @@ __device__ __forceinline__ void load_scales(const ScaleSrc& s, int super, int ha
       const bool in = int(first) + 4 * t < s.n_bytes;
       const uint32_t o = in ? first + 4 * t : 0u;
 #pragma unroll
-      for (int i = 0; i < 2 * kT; ++i) {
-        const uint8_t* base = s.base[i < kT ? 0 : (GLU && i % kT >= 2 ? 2 : 1)];
-        const int v = *reinterpret_cast<const int*>(base + ((i < kT ? s.a_off[i % kT] : s.b_off[i % kT]) + o));
+      for (int i = 0; i < MT + kT; ++i) {
+        const uint8_t* base = s.base[i < MT ? 0 : (GLU && i - MT >= 2 ? 2 : 1)];
+        const int v = *reinterpret_cast<const int*>(base + ((i < MT ? s.a_off[i] : s.b_off[i - MT]) + o));
         raw[i][t] = in ? v : 0;
       }
     }
   }
 }
 // raw: lane half h holds dwords 4h..4h+3 of the 8; stage t wants dword 2t + h
-__device__ __forceinline__ void spread_scales(const int (&raw)[2 * kT][4], Scales& s) {
+template <int MT>
+__device__ __forceinline__ void spread_scales(const int (&raw)[MT + kT][4], Scales<MT>& s) {
 #pragma unroll
-  for (int i = 0; i < 2 * kT; ++i) {
+  for (int i = 0; i < MT + kT; ++i) {
     const auto x = __builtin_amdgcn_permlane32_swap(raw[i][0], raw[i][1], false, false);
     const auto y = __builtin_amdgcn_permlane32_swap(raw[i][2], raw[i][3], false, false);
-    int(&d0)[kT] = i < kT ? s.a[0] : s.b[0];
-    int(&d1)[kT] = i < kT ? s.a[1] : s.b[1];
-    int(&d2)[kT] = i < kT ? s.a[2] : s.b[2];
-    int(&d3)[kT] = i < kT ? s.a[3] : s.b[3];
-    d0[i % kT] = x[0]; d2[i % kT] = x[1];
-    d1[i % kT] = y[0]; d3[i % kT] = y[1];
+    const int d[4] = {int(x[0]), int(y[0]), int(x[1]), int(y[1])};
+#pragma unroll
+    for (int t = 0; t < 4; ++t) (i < MT ? s.a[t][i < MT ? i : 0] : s.b[t][i < MT ? 0 : i - MT]) = d[t];
   }
 }
 
@@ -535,34 +540,35 @@ __device__ __forceinline__ void stage_barrier() {
 // SCALES: the scales of the next four stages are asked for in slice 1, younger
 // than all that this stage's barrier waits for, so that they have until the next
 // one (16384 rows, K 14336, N 4096: 544 -> 526 us).
-template <bool GLU, int T, int LEFT, bool SCALES = false>
-__device__ __forceinline__ void stage(f32x16 (&acc)[kT][kT], Frag& f0, Frag& f1, unsigned char* cur,
+template <bool GLU, int T, int LEFT, bool SCALES, int MT>
+__device__ __forceinline__ void stage(f32x16 (&acc)[MT][kT], Frag<MT>& f0, Frag<MT>& f1, unsigned char* cur,
                                       unsigned char* nxt, const Src& src, const Lds& l,
-                                      const Scales& sc, int wave, int d, const ScaleSrc& ss, int half,
-                                      int (&raw)[2 * kT][4]) {
+                                      const Scales<MT>& sc, int wave, int d, const ScaleSrc& ss, int half,
+                                      int (&raw)[MT + kT][4]) {
+  constexpr int kRows = 2 * MT, kReads = MT + kT;
   __builtin_amdgcn_sched_barrier(0);
-  if (LEFT > 0) load_runs<GLU, kLd, 2 * kLd>(nxt, src, wave, d + 1);
+  if (LEFT > 0) load_runs<GLU, MT, kRows, kRows + kLd>(nxt, src, wave, d + 1);
   read_frag(cur, l, 1, f1);
   mma<0>(acc, f0, sc.a[T], sc.b[T]);
-  slice_order<2 * kT, (LEFT > 0 ? kLd : 0)>();
+  slice_order<MT, kReads, (LEFT > 0 ? kLd : 0)>();
   __builtin_amdgcn_sched_barrier(0);
-  if (SCALES) load_scales<GLU, true>(ss, (d >> 2) + 1, half, raw);
+  if (SCALES) load_scales<GLU, true, MT>(ss, (d >> 2) + 1, half, raw);
   read_frag(cur, l, 2, f0);
   mma<1>(acc, f1, sc.a[T], sc.b[T]);
-  slice_order<2 * kT, (SCALES ? 2 * kT : 0)>();
+  slice_order<MT, kReads, (SCALES ? kReads : 0)>();
   __builtin_amdgcn_sched_barrier(0);
   read_frag(cur, l, 3, f1);
   mma<2>(acc, f0, sc.a[T], sc.b[T]);
-  slice_order<2 * kT, 0>();
+  slice_order<MT, kReads, 0>();
   __builtin_amdgcn_sched_barrier(0);
   if (LEFT > 0) {
-    stage_barrier<SCALES ? 2 * kT : 0>();   // stage d + 1 landed everywhere; cur is free
+    stage_barrier<SCALES ? kReads : 0>();   // stage d + 1 landed everywhere; cur is free
     __builtin_amdgcn_sched_barrier(0);
-    if (LEFT > 1) load_runs<GLU, 0, kLd>(cur, src, wave, d + 2);
+    if (LEFT > 1) load_runs<GLU, MT, 0, kRows>(cur, src, wave, d + 2);
     read_frag(nxt, l, 0, f0);
   }
   mma<3>(acc, f1, sc.a[T], sc.b[T]);
-  slice_order<(LEFT > 0 ? 2 * kT : 0), (LEFT > 1 ? kLd : 0)>();
+  slice_order<MT, (LEFT > 0 ? kReads : 0), (LEFT > 1 ? kRows : 0)>();
   __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -572,6 +578,116 @@ __device__ int count_tiles(const int32_t* __restrict__ offs, int n_experts, int 
   for (int c = 0; c < n_experts; c += Experts<kBM>::kPer * kWave)
     total += lane_value(wave_inclusive_scan(Experts<kBM>(c, offs, n_experts, n_rows).sum), kWave - 1);
   return __builtin_amdgcn_readfirstlane(total);
+}
+
+template <bool GLU, int TAIL, bool FULL, int MT>
+__device__ __forceinline__ void tile(const uint8_t* __restrict__ rows, const uint8_t* __restrict__ row_scales,
+                                     int K, const uint8_t* __restrict__ w, const uint8_t* __restrict__ w_scales,
+                                     const uint8_t* __restrict__ w_up, const uint8_t* __restrict__ w_up_scales,
+                                     int N, uint16_t* __restrict__ y, const Tile& t, int n_tile,
+                                     unsigned char* slot0, unsigned char* slot1) {
+  constexpr int kCols = GLU ? kBN / 2 : kBN;     // output columns of a tile
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
+  const int wm = wave >> 1, wn = wave & 1, r32 = lane & 31, half = lane >> 5;
+  const int64_t col0 = int64_t(n_tile) * kCols;
+  const int64_t w_row0 = int64_t(t.expert) * N + col0;
+  const int cols = N - int(col0);                // columns left, at least 1
+  const int left = t.row_end - t.row0;           // rows left, at least 1
+
+  Src src;
+  src.n_stages = (K + 255) / 256;
+  src.base[0] = rows + int64_t(t.row0) * (K / 2);
+  src.base[1] = w + w_row0 * (K / 2);
+  src.base[2] = GLU ? w_up + w_row0 * (K / 2) : nullptr;
+  const int q8 = lane >> 3;
+  const int chunk = (lane & 7) ^ ((4 * wave + (q8 >> 1)) & 7);
+  src.back = K % 256 != 0 && chunk >= 4 ? 64u : 0u;
+#pragma unroll
+  for (int i = 0; i < kLd; ++i) {
+    const int row = (4 * i + wave) * 8 + q8;
+    const int ar = row < left ? row : left - 1;            // clamped rows are never stored
+    const int bc = GLU ? row & (kCols - 1) : row;
+    const int br = bc < cols ? bc : cols - 1;
+    src.a_off[i] = uint32_t(ar) * uint32_t(K / 2) + chunk * 16;
+    src.b_off[i] = uint32_t(br) * uint32_t(K / 2) + chunk * 16;
+  }
+  // B tile rows of fragment j: columns wn*128 + 32 j, or with SwiGLU columns
+  // wn*64 + 32 (j % 2) of w (j < 2) and of w_up
+  Lds l;
+  ScaleSrc ss;
+  ss.n_bytes = K / 32;
+  ss.base[0] = row_scales + int64_t(t.row0) * ss.n_bytes;
+  ss.base[1] = w_scales + w_row0 * ss.n_bytes;
+  ss.base[2] = GLU ? w_up_scales + w_row0 * ss.n_bytes : nullptr;
+  l.a_row = (wm * 32 * MT + r32) * kRowBytes;
+#pragma unroll
+  for (int i = 0; i < kT; ++i) {
+    const int ar = wm * 32 * MT + 32 * i + r32;
+    const int bc = (GLU ? wn * 64 + 32 * (i & 1) : wn * 128 + 32 * i) + r32;
+    l.b_row[i] = ((GLU && i >= 2 ? kCols : 0) + bc) * kRowBytes;
+    ss.a_off[i] = uint32_t(ar < left ? ar : left - 1) * uint32_t(ss.n_bytes);
+    ss.b_off[i] = uint32_t(bc < cols ? bc : cols - 1) * uint32_t(ss.n_bytes);
+  }
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) l.chunk[kk] = ((4 * half + kk) ^ ((r32 >> 1) & 7)) << 4;
+
+  f32x16 acc[MT][kT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < kT; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+
+  Frag<MT> f0, f1;
+  Scales<MT> sc;
+  int raw[MT + kT][4];
+  load_runs<GLU, MT, 0, 2 * MT + kLd>(slot0, src, wave, 0);
+  load_scales<GLU, FULL, MT>(ss, 0, half, raw);
+  stage_barrier();                               // stage 0 landed
+  const int n_stages = src.n_stages;
+  if (n_stages > 1) load_runs<GLU, MT, 0, 2 * MT>(slot1, src, wave, 1);
+  read_frag(slot0, l, 0, f0);
+  int d = 0;
+  for (; d + TAIL < n_stages; d += 4) {
+    spread_scales(raw, sc);
+    if (!FULL) load_scales<GLU, false, MT>(ss, (d >> 2) + 1, half, raw);
+    stage<GLU, 0, 2, FULL, MT>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d, ss, half, raw);
+    stage<GLU, 1, 2, false, MT>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 1, ss, half, raw);
+    stage<GLU, 2, 2, false, MT>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d + 2, ss, half, raw);
+    stage<GLU, 3, 2, false, MT>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 3, ss, half, raw);
+  }
+  spread_scales(raw, sc);
+  stage<GLU, 0, TAIL - 1, false, MT>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d, ss, half, raw);
+  if constexpr (TAIL > 1) stage<GLU, 1, TAIL - 2, false, MT>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 1, ss, half, raw);
+  if constexpr (TAIL > 2) stage<GLU, 2, TAIL - 3, false, MT>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d + 2, ss, half, raw);
+  if constexpr (TAIL > 3) stage<GLU, 3, 0, false, MT>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 3, ss, half, raw);
+  __builtin_amdgcn_s_waitcnt(wait_vm(0));        // no direct load may outlive the workgroup
+  // the products end here, with every lane on, not in the divergent stores below
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < kT; ++j) asm volatile("" : "+a"(acc[i][j]));
+
+  // lane holds columns 8*(v/4) + 4*half + v%4 of row lane % 32 of each 32 x 32 tile
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int r = wm * 32 * MT + 32 * i + r32;
+    if (r >= left) continue;
+    uint16_t* out = y + int64_t(t.row0 + r) * N + col0;
+#pragma unroll
+    for (int j = 0; j < (GLU ? 2 : kT); ++j)
+#pragma unroll
+      for (int v = 0; v < 16; v += 4) {
+        const int c = (GLU ? wn * 64 : wn * 128) + 32 * j + 2 * v + 4 * half;
+        float o[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          o[u] = GLU ? silu(acc[i][j][v + u]) * acc[i][j + (GLU ? 2 : 0)][v + u] : acc[i][j][v + u];
+        store4(out, c, cols, N % 4 == 0, o);
+      }
+  }
 }
 
 // TAIL: the stages of the last group of up to four, each count its own straight
@@ -609,109 +725,13 @@ void tile_kernel(const uint8_t* __restrict__ rows, const uint8_t* __restrict__ r
   const Tile t = find_tile<kBM>(g * kGroupM + in_group % gm, offs, n_experts, n_rows);
   if (!t.valid) return;
   const int n_tile = in_group / gm;
-
-  constexpr int kCols = GLU ? kBN / 2 : kBN;     // output columns of a tile
-  const int lane = lane_id();
-  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
-  const int wm = wave >> 1, wn = wave & 1, r32 = lane & 31, half = lane >> 5;
-  const int64_t col0 = int64_t(n_tile) * kCols;
-  const int64_t w_row0 = int64_t(t.expert) * N + col0;
-  const int cols = N - int(col0);                // columns left, at least 1
-  const int left = t.row_end - t.row0;           // rows left, at least 1
-
-  Src src;
-  src.n_stages = (K + 255) / 256;
-  src.base[0] = rows + int64_t(t.row0) * (K / 2);
-  src.base[1] = w + w_row0 * (K / 2);
-  src.base[2] = GLU ? w_up + w_row0 * (K / 2) : nullptr;
-  const int q8 = lane >> 3;
-  const int chunk = (lane & 7) ^ ((4 * wave + (q8 >> 1)) & 7);
-  src.back = K % 256 != 0 && chunk >= 4 ? 64u : 0u;
-#pragma unroll
-  for (int i = 0; i < kLd; ++i) {
-    const int row = (4 * i + wave) * 8 + q8;
-    const int ar = row < left ? row : left - 1;            // clamped rows are never stored
-    const int bc = GLU ? row & (kCols - 1) : row;
-    const int br = bc < cols ? bc : cols - 1;
-    src.a_off[i] = uint32_t(ar) * uint32_t(K / 2) + chunk * 16;
-    src.b_off[i] = uint32_t(br) * uint32_t(K / 2) + chunk * 16;
-  }
-  // B tile rows of fragment j: columns wn*128 + 32 j, or with SwiGLU columns
-  // wn*64 + 32 (j % 2) of w (j < 2) and of w_up
-  Lds l;
-  ScaleSrc ss;
-  ss.n_bytes = K / 32;
-  ss.base[0] = row_scales + int64_t(t.row0) * ss.n_bytes;
-  ss.base[1] = w_scales + w_row0 * ss.n_bytes;
-  ss.base[2] = GLU ? w_up_scales + w_row0 * ss.n_bytes : nullptr;
-  l.a_row = (wm * 128 + r32) * kRowBytes;
-#pragma unroll
-  for (int i = 0; i < kT; ++i) {
-    const int ar = wm * 128 + 32 * i + r32;
-    const int bc = (GLU ? wn * 64 + 32 * (i & 1) : wn * 128 + 32 * i) + r32;
-    l.b_row[i] = ((GLU && i >= 2 ? kCols : 0) + bc) * kRowBytes;
-    ss.a_off[i] = uint32_t(ar < left ? ar : left - 1) * uint32_t(ss.n_bytes);
-    ss.b_off[i] = uint32_t(bc < cols ? bc : cols - 1) * uint32_t(ss.n_bytes);
-  }
-#pragma unroll
-  for (int kk = 0; kk < 4; ++kk) l.chunk[kk] = ((4 * half + kk) ^ ((r32 >> 1) & 7)) << 4;
-
-  f32x16 acc[kT][kT];
-#pragma unroll
-  for (int i = 0; i < kT; ++i)
-#pragma unroll
-    for (int j = 0; j < kT; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-
-  Frag f0, f1;
-  Scales sc;
-  int raw[2 * kT][4];
-  load_runs<GLU, 0, 2 * kLd>(slot0, src, wave, 0);
-  load_scales<GLU, FULL>(ss, 0, half, raw);
-  stage_barrier();                               // stage 0 landed
-  const int n_stages = src.n_stages;
-  if (n_stages > 1) load_runs<GLU, 0, kLd>(slot1, src, wave, 1);
-  read_frag(slot0, l, 0, f0);
-  int d = 0;
-  for (; d + TAIL < n_stages; d += 4) {
-    spread_scales(raw, sc);
-    if (!FULL) load_scales<GLU, false>(ss, (d >> 2) + 1, half, raw);
-    stage<GLU, 0, 2, FULL>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d, ss, half, raw);
-    stage<GLU, 1, 2>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 1, ss, half, raw);
-    stage<GLU, 2, 2>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d + 2, ss, half, raw);
-    stage<GLU, 3, 2>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 3, ss, half, raw);
-  }
-  spread_scales(raw, sc);
-  stage<GLU, 0, TAIL - 1>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d, ss, half, raw);
-  if constexpr (TAIL > 1) stage<GLU, 1, TAIL - 2>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 1, ss, half, raw);
-  if constexpr (TAIL > 2) stage<GLU, 2, TAIL - 3>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d + 2, ss, half, raw);
-  if constexpr (TAIL > 3) stage<GLU, 3, 0>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 3, ss, half, raw);
-  __builtin_amdgcn_s_waitcnt(wait_vm(0));        // no direct load may outlive the workgroup
-  // the products end here, with every lane on, not in the divergent stores below
-#pragma unroll
-  for (int i = 0; i < kT; ++i)
-#pragma unroll
-    for (int j = 0; j < kT; ++j) asm volatile("" : "+a"(acc[i][j]));
-
-  // lane holds columns 8*(v/4) + 4*half + v%4 of row lane % 32 of each 32 x 32 tile
-#pragma unroll
-  for (int i = 0; i < kT; ++i) {
-    const int r = wm * 128 + 32 * i + r32;
-    if (r >= left) continue;
-    uint16_t* out = y + int64_t(t.row0 + r) * N + col0;
-#pragma unroll
-    for (int j = 0; j < (GLU ? 2 : kT); ++j)
-#pragma unroll
-      for (int v = 0; v < 16; v += 4) {
-        const int c = (GLU ? wn * 64 : wn * 128) + 32 * j + 2 * v + 4 * half;
-        float o[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          o[u] = GLU ? silu(acc[i][j][v + u]) * acc[i][j + (GLU ? 2 : 0)][v + u] : acc[i][j][v + u];
-        store4(out, c, cols, N % 4 == 0, o);
-      }
-  }
+  const auto run = [&](auto mt) {
+    tile<GLU, TAIL, FULL, decltype(mt)::value>(rows, row_scales, K, w, w_scales, w_up, w_up_scales, N, y, t, n_tile, slot0, slot1);
+  };
+  const int left = t.row_end - t.row0;
+  if (left > 192) run(std::integral_constant<int, 4>());
+  else if (left > 128) run(std::integral_constant<int, 3>());
+  else run(std::integral_constant<int, 2>());
 }
 
 }  // namespace big
