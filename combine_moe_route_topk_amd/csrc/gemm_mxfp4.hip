@@ -373,7 +373,12 @@ __global__ __launch_bounds__(WAVES * kWave) void stream_kernel(
 // 256 x 256 tiles (SwiGLU: 128 columns of w and the same 128 of w_up), one
 // workgroup of 4 waves (2 x 2) per CU, a wave owning 128 x 128 as 4 x 4 MFMA
 // tiles whose 256 accumulators stay in registers: each operand byte read from
-// LDS feeds four MFMAs, half the LDS rate.
+// LDS feeds four MFMAs, half the LDS rate.  A tile that holds at most 192 or 128
+// rows (an expert's last) loads and multiplies only those: 3 or 2 row tiles a
+// wave (256 experts, K 7168, N 4096: 64 rows each 1012 -> 897 us; SwiGLU of N
+// 2048, 128 rows each 1087 -> 990).  Where the tiles are no more than half the
+// CUs, they have half the columns (8 experts of 64 rows, K = N = 4096: 22.0 ->
+// 17.2 us; 128 rows 27.1 -> 21.4; past half, 192 tiles, 37 -> 44, so not there).
 //   * K advances in stages of 256, so a stage row is 128 bytes of codes, one
 //     line.  Direct global->LDS loads fill two 64 KB slots: stage d is
 //     multiplied from slot d % 2 while stage d + 1 lands in the other; the one
@@ -391,13 +396,15 @@ __global__ __launch_bounds__(WAVES * kWave) void stream_kernel(
 namespace big {
 
 constexpr int kThreads = 256;
-constexpr int kBM = 256, kBN = 256;
+constexpr int kBM = 256;
 constexpr int kRowBytes = 128;                 // 256 codes
 constexpr int kTileBytes = kBM * kRowBytes;    // 32 KB per operand and stage
 constexpr int kSlotBytes = 2 * kTileBytes;
-constexpr int kLd = kTileBytes / (kThreads * 16);   // direct loads per lane and stage for the columns (8)
-constexpr int kT = 4;                          // 32-column MFMA tiles of a wave; MT of 32 rows: 4, or 2
-                                               // for a tile of at most 128 rows
+constexpr int kLd = kTileBytes / (kThreads * 16);   // direct loads per lane, operand and stage at most (8)
+// A wave has MT x NT MFMA tiles of 32 x 32: MT 4, 3 or 2; NT 4, or 2 where tiles
+// are few.
+constexpr int kT = 4;
+constexpr int64_t kFewTiles = 128;             // half the CUs
 constexpr int kGroupM = 8;                     // row tiles per group of the tile order
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
@@ -419,7 +426,7 @@ struct Src {
   int n_stages;
 };
 
-template <bool GLU, int MT, int LO, int HI>   // runs 0 .. 2 MT - 1: rows, the kLd after: columns
+template <bool GLU, int MT, int NT, int LO, int HI>   // runs 0 .. 2 MT - 1: rows, the 2 NT after: columns
 __device__ __forceinline__ void load_runs(unsigned char* slot, const Src& s, int wave, int d) {
   constexpr int kRows = 2 * MT;
   const bool last = d >= s.n_stages - 1;        // stages past the end repeat the last one
@@ -428,72 +435,71 @@ __device__ __forceinline__ void load_runs(unsigned char* slot, const Src& s, int
 #pragma unroll
   for (int i = LO; i < HI; ++i) {
     const int run = ((i < kRows ? i : i - kRows) * 4 + wave) * 1024;
-    const uint8_t* base = (i < kRows ? s.base[0] : s.base[GLU && i - kRows >= kLd / 2 ? 2 : 1]) + k;
+    const uint8_t* base = (i < kRows ? s.base[0] : s.base[GLU && i - kRows >= NT ? 2 : 1]) + k;
     const uint32_t o = (i < kRows ? s.a_off[i] : s.b_off[i - kRows]) - back;
     __builtin_amdgcn_global_load_lds(base + o, (lds_ptr)(slot + (i < kRows ? 0 : kTileBytes) + run), 16, 0, 0);
   }
 }
 
-template <int MT>
+template <int MT, int NT>
 struct Frag {
-  i32x4 a[MT], b[kT];
+  i32x4 a[MT], b[NT];
 };
 struct Lds {
   int a_row, b_row[kT], chunk[4];
 };
-template <int MT>
-__device__ __forceinline__ void read_frag(const unsigned char* slot, const Lds& l, int kk, Frag<MT>& f) {
+template <int MT, int NT>
+__device__ __forceinline__ void read_frag(const unsigned char* slot, const Lds& l, int kk, Frag<MT, NT>& f) {
 #pragma unroll
   for (int i = 0; i < MT; ++i)
     f.a[i] = *reinterpret_cast<const i32x4*>(slot + l.a_row + i * 32 * kRowBytes + l.chunk[kk]);
 #pragma unroll
-  for (int j = 0; j < kT; ++j)
+  for (int j = 0; j < NT; ++j)
     f.b[j] = *reinterpret_cast<const i32x4*>(slot + kTileBytes + l.b_row[j] + l.chunk[kk]);
 }
 
-template <int KK, int MT>
-__device__ __forceinline__ void mma(f32x16 (&acc)[MT][kT], const Frag<MT>& f, const int (&sa)[MT], const int (&sb)[kT]) {
+template <int KK, int MT, int NT>
+__device__ __forceinline__ void mma(f32x16 (&acc)[MT][NT], const Frag<MT, NT>& f, const int (&sa)[MT], const int (&sb)[NT]) {
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < kT; ++j) {
+    for (int j = 0; j < NT; ++j) {
       const i32x8 a = {f.a[i].x, f.a[i].y, f.a[i].z, f.a[i].w, 0, 0, 0, 0};
       const i32x8 b = {f.b[j].x, f.b[j].y, f.b[j].z, f.b[j].w, 0, 0, 0, 0};
       acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc[i][j], 4, 4, KK, sb[j], KK, sa[i]);
     }
 }
 
-// Issue order of one slice: its 4 MT MFMAs, the first R each followed by an LDS
+// Issue order of one slice: its M MFMAs, the first R each followed by an LDS
 // read, N direct loads spread between them.
-template <int MT, int R, int N>
+template <int M, int R, int N>
 __device__ __forceinline__ void slice_order() {
-  constexpr int kM = MT * kT;
-  static_assert(R <= kM && N <= kM, "at most one of each per MFMA");
+  static_assert(R <= M && N <= M, "at most one of each per MFMA");
 #pragma unroll
-  for (int q = 0; q < kM; ++q) {
+  for (int q = 0; q < M; ++q) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                     // MFMA
     if (q < R) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);          // LDS read
-    if ((q * N) / kM != ((q + 1) * N) / kM) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    if ((q * N) / M != ((q + 1) * N) / M) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
   }
 }
 
-// Scale dwords of four stages for MT rows and kT columns: [stage][row].
-template <int MT>
+// Scale dwords of four stages for MT rows and NT columns: [stage][row].
+template <int MT, int NT>
 struct Scales {
-  int a[4][MT], b[4][kT];
+  int a[4][MT], b[4][NT];
 };
 struct ScaleSrc {
   const uint8_t* base[3];
   uint32_t a_off[kT], b_off[kT];
   int n_bytes;                     // K / 32
 };
-template <bool GLU, bool FULL, int MT>   // FULL: the four stages are all within K
-__device__ __forceinline__ void load_scales(const ScaleSrc& s, int super, int half, int (&raw)[MT + kT][4]) {
+template <bool GLU, bool FULL, int MT, int NT>   // FULL: the four stages are all within K
+__device__ __forceinline__ void load_scales(const ScaleSrc& s, int super, int half, int (&raw)[MT + NT][4]) {
   const uint32_t first = 32 * super + 16 * half;
   if (FULL || 32 * super + 32 <= s.n_bytes) {
 #pragma unroll
-    for (int i = 0; i < MT + kT; ++i) {
-      const uint8_t* base = s.base[i < MT ? 0 : (GLU && i - MT >= 2 ? 2 : 1)];
+    for (int i = 0; i < MT + NT; ++i) {
+      const uint8_t* base = s.base[i < MT ? 0 : (GLU && i - MT >= NT / 2 ? 2 : 1)];
       const u32x4a q = *reinterpret_cast<const u32x4a*>(base + ((i < MT ? s.a_off[i] : s.b_off[i - MT]) + first));
       raw[i][0] = q.x; raw[i][1] = q.y; raw[i][2] = q.z; raw[i][3] = q.w;
     }
@@ -503,8 +509,8 @@ __device__ __forceinline__ void load_scales(const ScaleSrc& s, int super, int ha
       const bool in = int(first) + 4 * t < s.n_bytes;
       const uint32_t o = in ? first + 4 * t : 0u;
 #pragma unroll
-      for (int i = 0; i < MT + kT; ++i) {
-        const uint8_t* base = s.base[i < MT ? 0 : (GLU && i - MT >= 2 ? 2 : 1)];
+      for (int i = 0; i < MT + NT; ++i) {
+        const uint8_t* base = s.base[i < MT ? 0 : (GLU && i - MT >= NT / 2 ? 2 : 1)];
         const int v = *reinterpret_cast<const int*>(base + ((i < MT ? s.a_off[i] : s.b_off[i - MT]) + o));
         raw[i][t] = in ? v : 0;
       }
@@ -512,10 +518,10 @@ __device__ __forceinline__ void load_scales(const ScaleSrc& s, int super, int ha
   }
 }
 // raw: lane half h holds dwords 4h..4h+3 of the 8; stage t wants dword 2t + h
-template <int MT>
-__device__ __forceinline__ void spread_scales(const int (&raw)[MT + kT][4], Scales<MT>& s) {
+template <int MT, int NT>
+__device__ __forceinline__ void spread_scales(const int (&raw)[MT + NT][4], Scales<MT, NT>& s) {
 #pragma unroll
-  for (int i = 0; i < MT + kT; ++i) {
+  for (int i = 0; i < MT + NT; ++i) {
     const auto x = __builtin_amdgcn_permlane32_swap(raw[i][0], raw[i][1], false, false);
     const auto y = __builtin_amdgcn_permlane32_swap(raw[i][2], raw[i][3], false, false);
     const int d[4] = {int(x[0]), int(y[0]), int(x[1]), int(y[1])};
@@ -540,35 +546,35 @@ __device__ __forceinline__ void stage_barrier() {
 // SCALES: the scales of the next four stages are asked for in slice 1, younger
 // than all that this stage's barrier waits for, so that they have until the next
 // one (16384 rows, K 14336, N 4096: 544 -> 526 us).
-template <bool GLU, int T, int LEFT, bool SCALES, int MT>
-__device__ __forceinline__ void stage(f32x16 (&acc)[MT][kT], Frag<MT>& f0, Frag<MT>& f1, unsigned char* cur,
+template <bool GLU, int T, int LEFT, bool SCALES, int MT, int NT>
+__device__ __forceinline__ void stage(f32x16 (&acc)[MT][NT], Frag<MT, NT>& f0, Frag<MT, NT>& f1, unsigned char* cur,
                                       unsigned char* nxt, const Src& src, const Lds& l,
-                                      const Scales<MT>& sc, int wave, int d, const ScaleSrc& ss, int half,
-                                      int (&raw)[MT + kT][4]) {
-  constexpr int kRows = 2 * MT, kReads = MT + kT;
+                                      const Scales<MT, NT>& sc, int wave, int d, const ScaleSrc& ss, int half,
+                                      int (&raw)[MT + NT][4]) {
+  constexpr int kRows = 2 * MT, kColumns = 2 * NT, kReads = MT + NT, kM = MT * NT;
   __builtin_amdgcn_sched_barrier(0);
-  if (LEFT > 0) load_runs<GLU, MT, kRows, kRows + kLd>(nxt, src, wave, d + 1);
+  if (LEFT > 0) load_runs<GLU, MT, NT, kRows, kRows + kColumns>(nxt, src, wave, d + 1);
   read_frag(cur, l, 1, f1);
   mma<0>(acc, f0, sc.a[T], sc.b[T]);
-  slice_order<MT, kReads, (LEFT > 0 ? kLd : 0)>();
+  slice_order<kM, kReads, (LEFT > 0 ? kColumns : 0)>();
   __builtin_amdgcn_sched_barrier(0);
-  if (SCALES) load_scales<GLU, true, MT>(ss, (d >> 2) + 1, half, raw);
+  if (SCALES) load_scales<GLU, true, MT, NT>(ss, (d >> 2) + 1, half, raw);
   read_frag(cur, l, 2, f0);
   mma<1>(acc, f1, sc.a[T], sc.b[T]);
-  slice_order<MT, kReads, (SCALES ? kReads : 0)>();
+  slice_order<kM, kReads, (SCALES ? kReads : 0)>();
   __builtin_amdgcn_sched_barrier(0);
   read_frag(cur, l, 3, f1);
   mma<2>(acc, f0, sc.a[T], sc.b[T]);
-  slice_order<MT, kReads, 0>();
+  slice_order<kM, kReads, 0>();
   __builtin_amdgcn_sched_barrier(0);
   if (LEFT > 0) {
     stage_barrier<SCALES ? kReads : 0>();   // stage d + 1 landed everywhere; cur is free
     __builtin_amdgcn_sched_barrier(0);
-    if (LEFT > 1) load_runs<GLU, MT, 0, kRows>(cur, src, wave, d + 2);
+    if (LEFT > 1) load_runs<GLU, MT, NT, 0, kRows>(cur, src, wave, d + 2);
     read_frag(nxt, l, 0, f0);
   }
   mma<3>(acc, f1, sc.a[T], sc.b[T]);
-  slice_order<MT, (LEFT > 0 ? kReads : 0), (LEFT > 1 ? kRows : 0)>();
+  slice_order<kM, (LEFT > 0 ? kReads : 0), (LEFT > 1 ? kRows : 0)>();
   __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -580,13 +586,13 @@ __device__ int count_tiles(const int32_t* __restrict__ offs, int n_experts, int 
   return __builtin_amdgcn_readfirstlane(total);
 }
 
-template <bool GLU, int TAIL, bool FULL, int MT>
+template <bool GLU, int TAIL, bool FULL, int MT, int NT>
 __device__ __forceinline__ void tile(const uint8_t* __restrict__ rows, const uint8_t* __restrict__ row_scales,
                                      int K, const uint8_t* __restrict__ w, const uint8_t* __restrict__ w_scales,
                                      const uint8_t* __restrict__ w_up, const uint8_t* __restrict__ w_up_scales,
                                      int N, uint16_t* __restrict__ y, const Tile& t, int n_tile,
                                      unsigned char* slot0, unsigned char* slot1) {
-  constexpr int kCols = GLU ? kBN / 2 : kBN;     // output columns of a tile
+  constexpr int kCols = GLU ? 32 * NT : 64 * NT;   // output columns of a tile
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
   const int wm = wave >> 1, wn = wave & 1, r32 = lane & 31, half = lane >> 5;
@@ -624,51 +630,51 @@ __device__ __forceinline__ void tile(const uint8_t* __restrict__ rows, const uin
 #pragma unroll
   for (int i = 0; i < kT; ++i) {
     const int ar = wm * 32 * MT + 32 * i + r32;
-    const int bc = (GLU ? wn * 64 + 32 * (i & 1) : wn * 128 + 32 * i) + r32;
-    l.b_row[i] = ((GLU && i >= 2 ? kCols : 0) + bc) * kRowBytes;
+    const int bc = (GLU ? wn * 16 * NT + 32 * (i % (NT / 2)) : wn * 32 * NT + 32 * i) + r32;
+    l.b_row[i] = ((GLU && i >= NT / 2 ? kCols : 0) + bc) * kRowBytes;
     ss.a_off[i] = uint32_t(ar < left ? ar : left - 1) * uint32_t(ss.n_bytes);
     ss.b_off[i] = uint32_t(bc < cols ? bc : cols - 1) * uint32_t(ss.n_bytes);
   }
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk) l.chunk[kk] = ((4 * half + kk) ^ ((r32 >> 1) & 7)) << 4;
 
-  f32x16 acc[MT][kT];
+  f32x16 acc[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < kT; ++j)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
 
-  Frag<MT> f0, f1;
-  Scales<MT> sc;
-  int raw[MT + kT][4];
-  load_runs<GLU, MT, 0, 2 * MT + kLd>(slot0, src, wave, 0);
-  load_scales<GLU, FULL, MT>(ss, 0, half, raw);
+  Frag<MT, NT> f0, f1;
+  Scales<MT, NT> sc;
+  int raw[MT + NT][4];
+  load_runs<GLU, MT, NT, 0, 2 * MT + 2 * NT>(slot0, src, wave, 0);
+  load_scales<GLU, FULL, MT, NT>(ss, 0, half, raw);
   stage_barrier();                               // stage 0 landed
   const int n_stages = src.n_stages;
-  if (n_stages > 1) load_runs<GLU, MT, 0, 2 * MT>(slot1, src, wave, 1);
+  if (n_stages > 1) load_runs<GLU, MT, NT, 0, 2 * MT>(slot1, src, wave, 1);
   read_frag(slot0, l, 0, f0);
   int d = 0;
   for (; d + TAIL < n_stages; d += 4) {
     spread_scales(raw, sc);
-    if (!FULL) load_scales<GLU, false, MT>(ss, (d >> 2) + 1, half, raw);
-    stage<GLU, 0, 2, FULL, MT>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d, ss, half, raw);
-    stage<GLU, 1, 2, false, MT>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 1, ss, half, raw);
-    stage<GLU, 2, 2, false, MT>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d + 2, ss, half, raw);
-    stage<GLU, 3, 2, false, MT>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 3, ss, half, raw);
+    if (!FULL) load_scales<GLU, false, MT, NT>(ss, (d >> 2) + 1, half, raw);
+    stage<GLU, 0, 2, FULL, MT, NT>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d, ss, half, raw);
+    stage<GLU, 1, 2, false, MT, NT>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 1, ss, half, raw);
+    stage<GLU, 2, 2, false, MT, NT>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d + 2, ss, half, raw);
+    stage<GLU, 3, 2, false, MT, NT>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 3, ss, half, raw);
   }
   spread_scales(raw, sc);
-  stage<GLU, 0, TAIL - 1, false, MT>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d, ss, half, raw);
-  if constexpr (TAIL > 1) stage<GLU, 1, TAIL - 2, false, MT>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 1, ss, half, raw);
-  if constexpr (TAIL > 2) stage<GLU, 2, TAIL - 3, false, MT>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d + 2, ss, half, raw);
-  if constexpr (TAIL > 3) stage<GLU, 3, 0, false, MT>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 3, ss, half, raw);
+  stage<GLU, 0, TAIL - 1, false, MT, NT>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d, ss, half, raw);
+  if constexpr (TAIL > 1) stage<GLU, 1, TAIL - 2, false, MT, NT>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 1, ss, half, raw);
+  if constexpr (TAIL > 2) stage<GLU, 2, TAIL - 3, false, MT, NT>(acc, f0, f1, slot0, slot1, src, l, sc, wave, d + 2, ss, half, raw);
+  if constexpr (TAIL > 3) stage<GLU, 3, 0, false, MT, NT>(acc, f0, f1, slot1, slot0, src, l, sc, wave, d + 3, ss, half, raw);
   __builtin_amdgcn_s_waitcnt(wait_vm(0));        // no direct load may outlive the workgroup
   // the products end here, with every lane on, not in the divergent stores below
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < kT; ++j) asm volatile("" : "+a"(acc[i][j]));
+    for (int j = 0; j < NT; ++j) asm volatile("" : "+a"(acc[i][j]));
 
   // lane holds columns 8*(v/4) + 4*half + v%4 of row lane % 32 of each 32 x 32 tile
 #pragma unroll
@@ -677,14 +683,14 @@ __device__ __forceinline__ void tile(const uint8_t* __restrict__ rows, const uin
     if (r >= left) continue;
     uint16_t* out = y + int64_t(t.row0 + r) * N + col0;
 #pragma unroll
-    for (int j = 0; j < (GLU ? 2 : kT); ++j)
+    for (int j = 0; j < (GLU ? NT / 2 : NT); ++j)
 #pragma unroll
       for (int v = 0; v < 16; v += 4) {
-        const int c = (GLU ? wn * 64 : wn * 128) + 32 * j + 2 * v + 4 * half;
+        const int c = (GLU ? wn * 16 * NT : wn * 32 * NT) + 32 * j + 2 * v + 4 * half;
         float o[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          o[u] = GLU ? silu(acc[i][j][v + u]) * acc[i][j + (GLU ? 2 : 0)][v + u] : acc[i][j][v + u];
+          o[u] = GLU ? silu(acc[i][j][v + u]) * acc[i][j + (GLU ? NT / 2 : 0)][v + u] : acc[i][j][v + u];
         store4(out, c, cols, N % 4 == 0, o);
       }
   }
@@ -694,18 +700,19 @@ __device__ __forceinline__ void tile(const uint8_t* __restrict__ rows, const uin
 // line (exits in the middle of the four-stage loop made the compiler move the
 // accumulators).  FULL: K is a multiple of 1024, so scales are always read four
 // stages at a time (a branch for it inside a stage made the compiler spill).
+// FEW: the tiles can be few (FEW in every kernel cost 1% where they are not).
 // Measured: 16384 rows over 8 experts, K 4096, F 14336 with SwiGLU, 3.85 TFLOP
 // in 1.08 ms, 3.55 PFLOP/s; K 14336, N 4096 3.66 PFLOP/s.  The card's clock
 // falls to 1.4-1.9 GHz under it; at that clock MFMAs take 55% of the cycles of
 // a long K, the rest is waiting for operands.  With all codes zero, which draws
 // less power, the same calls run 12-16% faster.
-template <bool GLU, int TAIL, bool FULL>
+template <bool GLU, int TAIL, bool FULL, bool FEW>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void tile_kernel(const uint8_t* __restrict__ rows, const uint8_t* __restrict__ row_scales, int n_rows,
                  int K, const int32_t* __restrict__ offs, int n_experts,
                  const uint8_t* __restrict__ w, const uint8_t* __restrict__ w_scales,
                  const uint8_t* __restrict__ w_up, const uint8_t* __restrict__ w_up_scales, int N,
-                 uint16_t* __restrict__ y, int n_tiles) {
+                 uint16_t* __restrict__ y) {
   // two arrays, so the compiler can tell the slot being loaded from the slot
   // being read and adds no wait between them
   __shared__ __align__(1024) unsigned char slot0[kSlotBytes];
@@ -714,6 +721,9 @@ void tile_kernel(const uint8_t* __restrict__ rows, const uint8_t* __restrict__ r
   // XCD x (workgroup b runs on XCD b % 8) takes a contiguous range of the
   // grouped order: 8 row tiles x all column tiles, row tiles fastest
   const int m_real = count_tiles(offs, n_experts, n_rows);
+  constexpr int kWide = GLU ? 128 : 256;
+  const bool few = FEW && int64_t(m_real) * ((N + kWide - 1) / kWide) <= kFewTiles;
+  const int n_tiles = few ? (N + kWide / 2 - 1) / (kWide / 2) : (N + kWide - 1) / kWide;
   const int64_t tiles = int64_t(m_real) * n_tiles;
   const int64_t per_xcd = (tiles + kXcds - 1) / kXcds;
   const int64_t in_xcd = blockIdx.x / kXcds;
@@ -725,13 +735,20 @@ void tile_kernel(const uint8_t* __restrict__ rows, const uint8_t* __restrict__ r
   const Tile t = find_tile<kBM>(g * kGroupM + in_group % gm, offs, n_experts, n_rows);
   if (!t.valid) return;
   const int n_tile = in_group / gm;
-  const auto run = [&](auto mt) {
-    tile<GLU, TAIL, FULL, decltype(mt)::value>(rows, row_scales, K, w, w_scales, w_up, w_up_scales, N, y, t, n_tile, slot0, slot1);
+  const auto run = [&](auto mt, auto nt) {
+    tile<GLU, TAIL, FULL, decltype(mt)::value, decltype(nt)::value>(
+        rows, row_scales, K, w, w_scales, w_up, w_up_scales, N, y, t, n_tile, slot0, slot1);
   };
-  const int left = t.row_end - t.row0;
-  if (left > 192) run(std::integral_constant<int, 4>());
-  else if (left > 128) run(std::integral_constant<int, 3>());
-  else run(std::integral_constant<int, 2>());
+  const auto rows_of = [&](auto nt) {
+    const int left = t.row_end - t.row0;
+    if (left > 192) run(std::integral_constant<int, 4>(), nt);
+    else if (left > 128) run(std::integral_constant<int, 3>(), nt);
+    else run(std::integral_constant<int, 2>(), nt);
+  };
+  if constexpr (FEW) {
+    if (few) return rows_of(std::integral_constant<int, 2>());
+  }
+  rows_of(std::integral_constant<int, 4>());
 }
 
 }  // namespace big
@@ -755,12 +772,14 @@ GatherLayout gather_layout(int64_t n_rows, int n_experts) {
 }
 
 // Mean rows per expert from which tiles of 32 rows are taken, of 64 rows, and
-// the 256 x 256 kernel.  Measured (rows per expert: times in us of 16-, 32-,
-// 64-row tiles and the 256 x 256 kernel; 64 experts, K = N = 4096): 8: 104,
-// 108, 114, 144; 16: 138, 120, 116, 143; 32: 212, 148, 121, 149; 48: 288, 186,
-// 138, 160; 64: 366, 225, 163, 162; 128: 678, 393, 255, 179.  With 8 experts
-// 32-row tiles lead up to 24: 14.7 against 23.4 and 16.1.
-constexpr int64_t kNarrowRows = 10, kMiddleRows = 24, kManyRows = 64;
+// the tile kernel.  Measured (rows per expert: times in us of 16-, 32-, 64-row
+// tiles and the tile kernel; 64 experts, K = N = 4096): 8: 104, 108, 114, -; 16:
+// 138, 120, 116, -; 32: 212, 148, 121, 128; 48: 288, 186, 138, 136; 64: 366, 225,
+// 163, 141; 128: 678, 393, 255, 166.  256 experts, K 7168, N 4096: 40 rows 847
+// and 846, 56 rows 912 and 872.  With 8 experts 32-row tiles lead up to 24: 14.7
+// against 23.4 and 16.1; 64-row tiles and the tile kernel take 17.0 and 16.7 at
+// 48, 26.3 and 16.9 at 56.
+constexpr int64_t kNarrowRows = 10, kMiddleRows = 24, kManyRows = 48;
 
 // Row tiles at most: every expert can end in a partial one, and each holds a row.
 int64_t most_tiles(int64_t n_rows, int n_experts, int tm) {
@@ -775,6 +794,7 @@ constexpr int kStreamWaves = 4;    // 8 measured the same where rows are many, 2
 // The kernel that takes a product, and its grid.
 struct Shape {
   bool big, direct;
+  bool few;                        // big: the tiles can turn out to be few
   int nb;                          // stream: 16-row groups per tile
   int col_tiles;
   int64_t blocks;
@@ -787,6 +807,8 @@ Shape shape_of(const Mxfp4Product& g, bool gather) {
     const int cols = g.w_up ? 128 : 256;
     s.col_tiles = int((g.n_dim + cols - 1) / cols);
     s.blocks = most_tiles(rows, g.n_experts, big::kBM) * s.col_tiles;
+    s.few = (rows + big::kBM - 1) / big::kBM * s.col_tiles <= big::kFewTiles;
+    if (s.few && s.blocks < 2 * big::kFewTiles) s.blocks = 2 * big::kFewTiles;
     s.blocks = (s.blocks + kXcds - 1) / kXcds * kXcds;
     return s;
   }
@@ -807,7 +829,7 @@ hipError_t launch_product(const Mxfp4Product& g, const Shape& s, const int32_t* 
   const int n_rows = int(g.n_rows), k = int(g.k_dim), n = int(g.n_dim);
   const unsigned blocks = unsigned(s.blocks);
   auto big_kernel = [&](auto kernel) {
-    kernel<<<blocks, big::kThreads, 0, stream>>>(x, g.row_scales, n_rows, k, index, g.n_experts, w, g.w_scales, u, g.w_up_scales, n, y, s.col_tiles);
+    kernel<<<blocks, big::kThreads, 0, stream>>>(x, g.row_scales, n_rows, k, index, g.n_experts, w, g.w_scales, u, g.w_up_scales, n, y);
   };
   auto stream_kernel = [&](auto kernel) {
     kernel<<<blocks, kStreamWaves * kWave, 0, stream>>>(x, g.row_scales, n_rows, k, index, g.n_experts, order, w, g.w_scales, u, g.w_up_scales, n, y, s.col_tiles);
@@ -822,15 +844,17 @@ hipError_t launch_product(const Mxfp4Product& g, const Shape& s, const int32_t* 
   };
   auto go = [&](auto glu) {
     constexpr bool G = decltype(glu)::value;
-    if (s.big) {
-      if (k % 1024 == 0) return big_kernel(big::tile_kernel<G, 4, true>);
+    auto tiles = [&](auto few) {
+      constexpr bool F = decltype(few)::value;
+      if (k % 1024 == 0) return big_kernel(big::tile_kernel<G, 4, true, F>);
       switch ((k + 255) / 256 % 4) {
-        case 1: return big_kernel(big::tile_kernel<G, 1, false>);
-        case 2: return big_kernel(big::tile_kernel<G, 2, false>);
-        case 3: return big_kernel(big::tile_kernel<G, 3, false>);
-        default: return big_kernel(big::tile_kernel<G, 4, false>);
+        case 1: return big_kernel(big::tile_kernel<G, 1, false, F>);
+        case 2: return big_kernel(big::tile_kernel<G, 2, false, F>);
+        case 3: return big_kernel(big::tile_kernel<G, 3, false, F>);
+        default: return big_kernel(big::tile_kernel<G, 4, false, F>);
       }
-    }
+    };
+    if (s.big) return s.few ? tiles(std::true_type()) : tiles(std::false_type());
     if (k % 512 == 0) pick(glu, std::true_type());
     else pick(glu, std::false_type());
   };

@@ -279,6 +279,28 @@ def test_zero_rows():
     assert moe.moe_gather_gemm_mxfp4(z(0, 64), z(0, 4), i32(0), z(2, 8, 64), z(2, 8, 4)).shape == (0, 8)
 
 
+# tiles of up to 128, 192 and 256 rows; few of them in all (300 columns), none too
+# few (4200) and never few (6600); every number of K stages modulo 4, whole or not
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("n", [300, 4200, 6600])
+@pytest.mark.parametrize("k", [128, 384, 640, 1024, 1152, 1536, 2048, 2688])
+def test_tiles_of_every_height(k, n, glu):
+    rng = np.random.default_rng(k + n)
+    counts = [1, 130, 192, 300, 0, 128, 193, 512 + 129]
+    e, r = len(counts), sum(counts)
+    rows, rs = _operand(rng, r, k)
+    w = _operand(rng, e, n, k)
+    up = _operand(rng, e, n, k) if glu else None
+    if glu:
+        rs, w = (rs - np.uint8(4)).astype(np.uint8), (w[0], (w[1] - np.uint8(3)).astype(np.uint8))
+    ids = np.repeat(np.arange(e), counts).astype(np.int32)
+    y = to_np(_run("grouped", rows, rs, ids, w, up))
+    cols = np.unique(np.concatenate([np.arange(0, n, 61), np.arange(250, 260), np.arange(n - 70, n)]))
+    at = lambda m: None if m is None else (m[0][:, cols], m[1][:, cols])
+    with np.errstate(over="ignore"):
+        _check(y[:, cols], rows, rs, ids, at(w), at(up), f"K={k} N={n} glu={glu}")
+
+
 # at least 128 rows per expert: every number of 256-wide K stages modulo 4, with
 # and without a half stage at the end, row and column counts off the tile
 @pytest.mark.parametrize("glu", [False, True])
