@@ -590,8 +590,8 @@ template <bool GLU, int TAIL, bool FULL, int MT, int NT>
 __device__ __forceinline__ void tile(const uint8_t* __restrict__ rows, const uint8_t* __restrict__ row_scales,
                                      int K, const uint8_t* __restrict__ w, const uint8_t* __restrict__ w_scales,
                                      const uint8_t* __restrict__ w_up, const uint8_t* __restrict__ w_up_scales,
-                                     int N, uint16_t* __restrict__ y, const Tile& t, int n_tile,
-                                     unsigned char* slot0, unsigned char* slot1) {
+                                     int N, uint16_t* __restrict__ y, const int32_t* __restrict__ order,
+                                     const Tile& t, int n_tile, unsigned char* slot0, unsigned char* slot1) {
   constexpr int kCols = GLU ? 32 * NT : 64 * NT;   // output columns of a tile
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
@@ -600,10 +600,13 @@ __device__ __forceinline__ void tile(const uint8_t* __restrict__ rows, const uin
   const int64_t w_row0 = int64_t(t.expert) * N + col0;
   const int cols = N - int(col0);                // columns left, at least 1
   const int left = t.row_end - t.row0;           // rows left, at least 1
+  // row i of the tile, from row `first` of rows and of row_scales
+  const int first = order ? 0 : t.row0;
+  auto row_at = [&](int i) { return order ? order[t.row0 + i] : i; };
 
   Src src;
   src.n_stages = (K + 255) / 256;
-  src.base[0] = rows + int64_t(t.row0) * (K / 2);
+  src.base[0] = rows + int64_t(first) * (K / 2);
   src.base[1] = w + w_row0 * (K / 2);
   src.base[2] = GLU ? w_up + w_row0 * (K / 2) : nullptr;
   const int q8 = lane >> 3;
@@ -615,7 +618,7 @@ __device__ __forceinline__ void tile(const uint8_t* __restrict__ rows, const uin
     const int ar = row < left ? row : left - 1;            // clamped rows are never stored
     const int bc = GLU ? row & (kCols - 1) : row;
     const int br = bc < cols ? bc : cols - 1;
-    src.a_off[i] = uint32_t(ar) * uint32_t(K / 2) + chunk * 16;
+    src.a_off[i] = uint32_t(row_at(ar)) * uint32_t(K / 2) + chunk * 16;
     src.b_off[i] = uint32_t(br) * uint32_t(K / 2) + chunk * 16;
   }
   // B tile rows of fragment j: columns wn*128 + 32 j, or with SwiGLU columns
@@ -623,7 +626,7 @@ __device__ __forceinline__ void tile(const uint8_t* __restrict__ rows, const uin
   Lds l;
   ScaleSrc ss;
   ss.n_bytes = K / 32;
-  ss.base[0] = row_scales + int64_t(t.row0) * ss.n_bytes;
+  ss.base[0] = row_scales + int64_t(first) * ss.n_bytes;
   ss.base[1] = w_scales + w_row0 * ss.n_bytes;
   ss.base[2] = GLU ? w_up_scales + w_row0 * ss.n_bytes : nullptr;
   l.a_row = (wm * 32 * MT + r32) * kRowBytes;
@@ -632,7 +635,7 @@ __device__ __forceinline__ void tile(const uint8_t* __restrict__ rows, const uin
     const int ar = wm * 32 * MT + 32 * i + r32;
     const int bc = (GLU ? wn * 16 * NT + 32 * (i % (NT / 2)) : wn * 32 * NT + 32 * i) + r32;
     l.b_row[i] = ((GLU && i >= NT / 2 ? kCols : 0) + bc) * kRowBytes;
-    ss.a_off[i] = uint32_t(ar < left ? ar : left - 1) * uint32_t(ss.n_bytes);
+    ss.a_off[i] = uint32_t(row_at(ar < left ? ar : left - 1)) * uint32_t(ss.n_bytes);
     ss.b_off[i] = uint32_t(bc < cols ? bc : cols - 1) * uint32_t(ss.n_bytes);
   }
 #pragma unroll
@@ -681,7 +684,7 @@ __device__ __forceinline__ void tile(const uint8_t* __restrict__ rows, const uin
   for (int i = 0; i < MT; ++i) {
     const int r = wm * 32 * MT + 32 * i + r32;
     if (r >= left) continue;
-    uint16_t* out = y + int64_t(t.row0 + r) * N + col0;
+    uint16_t* out = y + int64_t(order ? order[t.row0 + r] : t.row0 + r) * N + col0;
 #pragma unroll
     for (int j = 0; j < (GLU ? NT / 2 : NT); ++j)
 #pragma unroll
@@ -696,20 +699,23 @@ __device__ __forceinline__ void tile(const uint8_t* __restrict__ rows, const uin
   }
 }
 
+// order: as in stream_kernel (rows * K / 2 below 2^32 then; only with ANY).
+// 16384 rows in any order over 8 experts, K = N = 4096: 205 us, 399 by 64-row tiles.
 // TAIL: the stages of the last group of up to four, each count its own straight
 // line (exits in the middle of the four-stage loop made the compiler move the
 // accumulators).  FULL: K is a multiple of 1024, so scales are always read four
 // stages at a time (a branch for it inside a stage made the compiler spill).
-// FEW: the tiles can be few (FEW in every kernel cost 1% where they are not).
+// ANY: the tiles can be few, or rows be in any order (in every kernel these cost
+// SwiGLU 1% and 2% where neither is so).
 // Measured: 16384 rows over 8 experts, K 4096, F 14336 with SwiGLU, 3.85 TFLOP
 // in 1.08 ms, 3.55 PFLOP/s; K 14336, N 4096 3.66 PFLOP/s.  The card's clock
 // falls to 1.4-1.9 GHz under it; at that clock MFMAs take 55% of the cycles of
 // a long K, the rest is waiting for operands.  With all codes zero, which draws
 // less power, the same calls run 12-16% faster.
-template <bool GLU, int TAIL, bool FULL, bool FEW>
+template <bool GLU, int TAIL, bool FULL, bool ANY>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void tile_kernel(const uint8_t* __restrict__ rows, const uint8_t* __restrict__ row_scales, int n_rows,
-                 int K, const int32_t* __restrict__ offs, int n_experts,
+                 int K, const int32_t* __restrict__ offs, int n_experts, const int32_t* __restrict__ order,
                  const uint8_t* __restrict__ w, const uint8_t* __restrict__ w_scales,
                  const uint8_t* __restrict__ w_up, const uint8_t* __restrict__ w_up_scales, int N,
                  uint16_t* __restrict__ y) {
@@ -722,7 +728,7 @@ void tile_kernel(const uint8_t* __restrict__ rows, const uint8_t* __restrict__ r
   // grouped order: 8 row tiles x all column tiles, row tiles fastest
   const int m_real = count_tiles(offs, n_experts, n_rows);
   constexpr int kWide = GLU ? 128 : 256;
-  const bool few = FEW && int64_t(m_real) * ((N + kWide - 1) / kWide) <= kFewTiles;
+  const bool few = ANY && int64_t(m_real) * ((N + kWide - 1) / kWide) <= kFewTiles;
   const int n_tiles = few ? (N + kWide / 2 - 1) / (kWide / 2) : (N + kWide - 1) / kWide;
   const int64_t tiles = int64_t(m_real) * n_tiles;
   const int64_t per_xcd = (tiles + kXcds - 1) / kXcds;
@@ -737,7 +743,7 @@ void tile_kernel(const uint8_t* __restrict__ rows, const uint8_t* __restrict__ r
   const int n_tile = in_group / gm;
   const auto run = [&](auto mt, auto nt) {
     tile<GLU, TAIL, FULL, decltype(mt)::value, decltype(nt)::value>(
-        rows, row_scales, K, w, w_scales, w_up, w_up_scales, N, y, t, n_tile, slot0, slot1);
+        rows, row_scales, K, w, w_scales, w_up, w_up_scales, N, y, ANY ? order : nullptr, t, n_tile, slot0, slot1);
   };
   const auto rows_of = [&](auto nt) {
     const int left = t.row_end - t.row0;
@@ -745,7 +751,7 @@ void tile_kernel(const uint8_t* __restrict__ rows, const uint8_t* __restrict__ r
     else if (left > 128) run(std::integral_constant<int, 3>(), nt);
     else run(std::integral_constant<int, 2>(), nt);
   };
-  if constexpr (FEW) {
+  if constexpr (ANY) {
     if (few) return rows_of(std::integral_constant<int, 2>());
   }
   rows_of(std::integral_constant<int, 4>());
@@ -794,7 +800,7 @@ constexpr int kStreamWaves = 4;    // 8 measured the same where rows are many, 2
 // The kernel that takes a product, and its grid.
 struct Shape {
   bool big, direct;
-  bool few;                        // big: the tiles can turn out to be few
+  bool any;                        // big: the tiles can turn out to be few, or rows are in any order
   int nb;                          // stream: 16-row groups per tile
   int col_tiles;
   int64_t blocks;
@@ -802,13 +808,15 @@ struct Shape {
 Shape shape_of(const Mxfp4Product& g, bool gather) {
   Shape s{};
   const int64_t rows = g.n_rows, e = g.n_experts;
-  s.big = !gather && rows >= kManyRows * e;
+  // rows in any order are 32-bit offsets from the first in the tile kernel
+  s.big = rows >= kManyRows * e && (!gather || rows * (g.k_dim / 2) < int64_t(1) << 32);
   if (s.big) {
     const int cols = g.w_up ? 128 : 256;
     s.col_tiles = int((g.n_dim + cols - 1) / cols);
     s.blocks = most_tiles(rows, g.n_experts, big::kBM) * s.col_tiles;
-    s.few = (rows + big::kBM - 1) / big::kBM * s.col_tiles <= big::kFewTiles;
-    if (s.few && s.blocks < 2 * big::kFewTiles) s.blocks = 2 * big::kFewTiles;
+    const bool few = (rows + big::kBM - 1) / big::kBM * s.col_tiles <= big::kFewTiles;
+    s.any = few || gather;
+    if (few && s.blocks < 2 * big::kFewTiles) s.blocks = 2 * big::kFewTiles;
     s.blocks = (s.blocks + kXcds - 1) / kXcds * kXcds;
     return s;
   }
@@ -829,7 +837,7 @@ hipError_t launch_product(const Mxfp4Product& g, const Shape& s, const int32_t* 
   const int n_rows = int(g.n_rows), k = int(g.k_dim), n = int(g.n_dim);
   const unsigned blocks = unsigned(s.blocks);
   auto big_kernel = [&](auto kernel) {
-    kernel<<<blocks, big::kThreads, 0, stream>>>(x, g.row_scales, n_rows, k, index, g.n_experts, w, g.w_scales, u, g.w_up_scales, n, y);
+    kernel<<<blocks, big::kThreads, 0, stream>>>(x, g.row_scales, n_rows, k, index, g.n_experts, order, w, g.w_scales, u, g.w_up_scales, n, y);
   };
   auto stream_kernel = [&](auto kernel) {
     kernel<<<blocks, kStreamWaves * kWave, 0, stream>>>(x, g.row_scales, n_rows, k, index, g.n_experts, order, w, g.w_scales, u, g.w_up_scales, n, y, s.col_tiles);
@@ -844,17 +852,17 @@ hipError_t launch_product(const Mxfp4Product& g, const Shape& s, const int32_t* 
   };
   auto go = [&](auto glu) {
     constexpr bool G = decltype(glu)::value;
-    auto tiles = [&](auto few) {
-      constexpr bool F = decltype(few)::value;
-      if (k % 1024 == 0) return big_kernel(big::tile_kernel<G, 4, true, F>);
+    auto tiles = [&](auto any) {
+      constexpr bool A = decltype(any)::value;
+      if (k % 1024 == 0) return big_kernel(big::tile_kernel<G, 4, true, A>);
       switch ((k + 255) / 256 % 4) {
-        case 1: return big_kernel(big::tile_kernel<G, 1, false, F>);
-        case 2: return big_kernel(big::tile_kernel<G, 2, false, F>);
-        case 3: return big_kernel(big::tile_kernel<G, 3, false, F>);
-        default: return big_kernel(big::tile_kernel<G, 4, false, F>);
+        case 1: return big_kernel(big::tile_kernel<G, 1, false, A>);
+        case 2: return big_kernel(big::tile_kernel<G, 2, false, A>);
+        case 3: return big_kernel(big::tile_kernel<G, 3, false, A>);
+        default: return big_kernel(big::tile_kernel<G, 4, false, A>);
       }
     };
-    if (s.big) return s.few ? tiles(std::true_type()) : tiles(std::false_type());
+    if (s.big) return s.any ? tiles(std::true_type()) : tiles(std::false_type());
     if (k % 512 == 0) pick(glu, std::true_type());
     else pick(glu, std::false_type());
   };

@@ -550,8 +550,8 @@ int moe_grouped_gemm_mxfp4(const uint8_t* rows, const uint8_t* row_scales, int64
 size_t moe_gather_gemm_mxfp4_workspace_bytes(int64_t n_rows, int32_t n_experts);
 
 /* moe_gather_gemm_mxfp4 -- the product of moe_grouped_gemm_mxfp4 over rows left
- * in any order, row r taking expert row_expert[r] (the unsorted dispatch;
- * meant for few rows per expert, as moe_gather_swiglu).  y[r] lands at row r;
+ * in any order, row r taking expert row_expert[r] (the unsorted dispatch).
+ * y[r] lands at row r;
  * rows whose id lies outside [0, E) leave y as it was.
  *   row_expert  [n_rows] int32, device-resident
  *   workspace   moe_gather_gemm_mxfp4_workspace_bytes(n_rows, E) bytes,

@@ -301,6 +301,28 @@ def test_tiles_of_every_height(k, n, glu):
         _check(y[:, cols], rows, rs, ids, at(w), at(up), f"K={k} N={n} glu={glu}")
 
 
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("k,n", [(384, 300), (640, 4200), (1024, 300), (1152, 700), (2048, 6600)])
+def test_many_rows_in_any_order(k, n, glu):
+    """Rows of every tile height in shuffled order, some without an expert."""
+    rng = np.random.default_rng(k + n + glu)
+    ids = rng.permutation(np.repeat([0, 1, 2, 3, 5, 6, 7, -1, 8], [1, 130, 192, 300, 128, 193, 641, 20, 9])).astype(np.int32)
+    e, r = 8, ids.size
+    rows, rs = _operand(rng, r, k)
+    w = _operand(rng, e, n, k)
+    up = _operand(rng, e, n, k) if glu else None
+    if glu:
+        rs, w = (rs - np.uint8(4)).astype(np.uint8), (w[0], (w[1] - np.uint8(3)).astype(np.uint8))
+    y = torch.full((r, n), 7.0, dtype=torch.bfloat16, device=DEV)
+    _run("gather", rows, rs, ids, w, up, y=y)
+    good = (ids >= 0) & (ids < e)
+    assert (as_f32(to_np(y))[~good] == 7).all()
+    cols = np.unique(np.concatenate([np.arange(0, n, 61), np.arange(250, 260), np.arange(n - 70, n)]))
+    at = lambda m: None if m is None else (m[0][:, cols], m[1][:, cols])
+    with np.errstate(over="ignore"):
+        _check(to_np(y)[good][:, cols], rows[good], rs[good], ids[good], at(w), at(up), f"K={k} N={n} glu={glu}")
+
+
 # at least 128 rows per expert: every number of 256-wide K stages modulo 4, with
 # and without a half stage at the end, row and column counts off the tile
 @pytest.mark.parametrize("glu", [False, True])
@@ -353,6 +375,22 @@ def test_weights_past_four_gibibytes():
     for y in (moe.moe_gather_gemm_mxfp4(rows, rs, ids, w, ws),
               moe.moe_grouped_gemm_mxfp4(rows, rs, torch.tensor([0] + [1] * (e - 1) + [r], dtype=torch.int32, device=DEV), w, ws)):
         assert bool((y[0] == 0).all()) and bool((y[1:] == k / 64).all())
+
+
+@pytest.mark.parametrize("r", [520_000, 530_000])
+def test_rows_in_any_order_past_four_gibibytes(r):
+    """Row offsets up to and beyond 2^32 bytes (8192 of codes a row)."""
+    k, n = 16384, 16
+    rows = torch.zeros((r, k // 2), dtype=torch.uint8, device=DEV)
+    rs = torch.full((r, k // 32), 121, dtype=torch.uint8, device=DEV)
+    w, ws = torch.full((2, n, k // 2), 0x22, dtype=torch.uint8, device=DEV), torch.full((2, n, k // 32), 127, dtype=torch.uint8, device=DEV)
+    ws[1] += 1
+    ids = torch.arange(r, dtype=torch.int32, device=DEV) % 2
+    hot = torch.tensor([0, 1, r // 2, r - 2, r - 1], device=DEV)
+    rows[hot] = 0x22
+    y = moe.moe_gather_gemm_mxfp4(rows, rs, ids, w, ws)
+    assert int((y != 0).any(1).sum()) == 5
+    assert torch.equal(y[hot], ((ids[hot] + 1) * (k // 64)).to(y.dtype).unsqueeze(1).expand(5, n))
 
 
 def test_refusals():
