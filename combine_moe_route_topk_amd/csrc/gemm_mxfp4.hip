@@ -10,6 +10,7 @@
 
 #include "device_common.hpp"
 #include "launch.hpp"
+#include "mxfp4_tiles.hpp"
 
 namespace moe {
 
@@ -396,7 +397,6 @@ __global__ __launch_bounds__(WAVES * kWave) void stream_kernel(
 namespace big {
 
 constexpr int kThreads = 256;
-constexpr int kBM = 256;
 constexpr int kRowBytes = 128;                 // 256 codes
 constexpr int kTileBytes = kBM * kRowBytes;    // 32 KB per operand and stage
 constexpr int kSlotBytes = 2 * kTileBytes;
@@ -404,7 +404,6 @@ constexpr int kLd = kTileBytes / (kThreads * 16);   // direct loads per lane, op
 // A wave has MT x NT MFMA tiles of 32 x 32: MT 4, 3 or 2; NT 4, or 2 where tiles
 // are few.
 constexpr int kT = 4;
-constexpr int64_t kFewTiles = 128;             // half the CUs
 constexpr int kGroupM = 8;                     // row tiles per group of the tile order
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
@@ -727,9 +726,8 @@ void tile_kernel(const uint8_t* __restrict__ rows, const uint8_t* __restrict__ r
   // XCD x (workgroup b runs on XCD b % 8) takes a contiguous range of the
   // grouped order: 8 row tiles x all column tiles, row tiles fastest
   const int m_real = count_tiles(offs, n_experts, n_rows);
-  constexpr int kWide = GLU ? 128 : 256;
-  const bool few = ANY && int64_t(m_real) * ((N + kWide - 1) / kWide) <= kFewTiles;
-  const int n_tiles = few ? (N + kWide / 2 - 1) / (kWide / 2) : (N + kWide - 1) / kWide;
+  const bool few = few_tiles(m_real, N, GLU, ANY);
+  const int n_tiles = int(col_tiles(N, GLU, few));
   const int64_t tiles = int64_t(m_real) * n_tiles;
   const int64_t per_xcd = (tiles + kXcds - 1) / kXcds;
   const int64_t in_xcd = blockIdx.x / kXcds;
@@ -802,7 +800,7 @@ struct Shape {
   bool big, direct;
   bool any;                        // big: the tiles can turn out to be few, or rows are in any order
   int nb;                          // stream: 16-row groups per tile
-  int col_tiles;
+  int col_tiles;                   // stream: column groups
   int64_t blocks;
 };
 Shape shape_of(const Mxfp4Product& g, bool gather) {
@@ -811,13 +809,9 @@ Shape shape_of(const Mxfp4Product& g, bool gather) {
   // rows in any order are 32-bit offsets from the first in the tile kernel
   s.big = rows >= kManyRows * e && (!gather || rows * (g.k_dim / 2) < int64_t(1) << 32);
   if (s.big) {
-    const int cols = g.w_up ? 128 : 256;
-    s.col_tiles = int((g.n_dim + cols - 1) / cols);
-    s.blocks = most_tiles(rows, g.n_experts, big::kBM) * s.col_tiles;
-    const bool few = (rows + big::kBM - 1) / big::kBM * s.col_tiles <= big::kFewTiles;
-    s.any = few || gather;
-    if (few && s.blocks < 2 * big::kFewTiles) s.blocks = 2 * big::kFewTiles;
-    s.blocks = (s.blocks + kXcds - 1) / kXcds * kXcds;
+    s.any = gather || big::few_tiles((rows + big::kBM - 1) / big::kBM, g.n_dim, g.w_up, true);
+    s.blocks = big::blocks_for(most_tiles(rows, g.n_experts, big::kBM), g.n_dim, g.w_up, s.any);
+    s.blocks = (s.blocks + kXcds - 1) / kXcds * kXcds;   // every XCD as many
     return s;
   }
   s.nb = rows < kNarrowRows * e ? 1 : (rows < kMiddleRows * e ? 2 : 4);
