@@ -192,11 +192,48 @@ hipError_t launch_combine_backward_typed(const void* d_out, const void* y, int64
   return hipGetLastError();
 }
 
+// v of the lane that DPP control CTRL names; v itself where that lane or this
+// one's row takes no part.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ float dpp_or_self(float v) {
+  const int b = __float_as_int(v);
+  return __int_as_float(__builtin_amdgcn_update_dpp(b, b, CTRL, ROW_MASK, 0xF, false));
+}
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ float dpp_or_zero(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROW_MASK, 0xF, true));
+}
+__device__ __forceinline__ float lane63(float v) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+// Maximum and sum over the wave by DPP row operations (within quads, halves and
+// rows of 16 lanes, then across the rows), the same in every lane.
+__device__ __forceinline__ float wave_max_dpp(float v) {
+  v = fmaxf(v, dpp_or_self<0xB1, 0xF>(v));      // lanes 1 0 3 2
+  v = fmaxf(v, dpp_or_self<0x4E, 0xF>(v));      // lanes 2 3 0 1
+  v = fmaxf(v, dpp_or_self<0x141, 0xF>(v));     // row_half_mirror
+  v = fmaxf(v, dpp_or_self<0x140, 0xF>(v));     // row_mirror
+  v = fmaxf(v, dpp_or_self<0x142, 0xA>(v));     // row_bcast:15
+  v = fmaxf(v, dpp_or_self<0x143, 0xC>(v));     // row_bcast:31
+  return lane63(v);
+}
+__device__ __forceinline__ float wave_sum_dpp(float v) {
+  v += dpp_or_zero<0xB1, 0xF>(v);
+  v += dpp_or_zero<0x4E, 0xF>(v);
+  v += dpp_or_zero<0x141, 0xF>(v);
+  v += dpp_or_zero<0x140, 0xF>(v);
+  v += dpp_or_zero<0x142, 0xA>(v);
+  v += dpp_or_zero<0x143, 0xC>(v);
+  return lane63(v);
+}
+
 // One wave per token; lane l holds experts l, l + 64, ..., so a row is written
 // in whole 256-byte runs.  The slots are added in order j = 0..k-1, also where
-// two of them name the same expert.  RENORM false needs the full softmax
-// again: p_e = exp(l_e - l_r) w_r with r the first slot's expert, the largest
-// logit, whose weight w_r is 1 / sum exp(l - l_r); no pass for the sum.
+// two of them name the same expert.  RENORM false computes the softmax of the
+// row's logits again, p_e = exp(l_e - max) / sum exp(l - max), from registers.
+// The first slot's logit serves as the maximum where none is larger; that
+// expert may have been dropped, though, or the slots come in another order, and
+// then the lanes exchange theirs (always: 15.2 -> 16.2 us for 32768 x 256).
 template <int SLOTS, bool RENORM>
 __global__ __launch_bounds__(kBlock) void route_backward_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
@@ -210,25 +247,34 @@ __global__ __launch_bounds__(kBlock) void route_backward_kernel(
   const bool ok = unsigned(my_e) < unsigned(n_experts);
   const float w = ok ? topk_w[t * k + lane] : 0.f;
   const float wd = ok ? w * d_w[t * k + lane] : 0.f;
-  float l[SLOTS], l_r = 0.f, w_r = 0.f;
+  float p[SLOTS];
   if (!RENORM) {
     const int e_r = __builtin_amdgcn_readfirstlane(my_e);
-    if (unsigned(e_r) < unsigned(n_experts)) {
-      l_r = logits[t * n_experts + e_r];
-      w_r = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(w)));
-    }
+    float mine_top = -__builtin_inff(), top = 0.f, total = 0.f;
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
       const int e = s * kWave + lane;
-      l[s] = e < n_experts ? logits[t * n_experts + e] : 0.f;
+      p[s] = e < n_experts ? logits[t * n_experts + e] : -__builtin_inff();
+      mine_top = fmaxf(mine_top, p[s]);
+      top = e_r / kWave == s ? p[s] : top;
     }
+    top = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(top), e_r & (kWave - 1)));
+    if (unsigned(e_r) >= unsigned(n_experts) || ballot(mine_top > top)) top = wave_max_dpp(mine_top);
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      p[s] = expf(p[s] - top);
+      total += p[s];
+    }
+    const float inv = 1.f / wave_sum_dpp(total);
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) p[s] *= inv;
   }
   float sum = 0.f;
   for (int j = 0; j < k; ++j) sum += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wd), j));
   const float mine = RENORM ? wd - w * sum : wd;
   float d[SLOTS];
 #pragma unroll
-  for (int s = 0; s < SLOTS; ++s) d[s] = RENORM ? 0.f : -(expf(l[s] - l_r) * w_r) * sum;
+  for (int s = 0; s < SLOTS; ++s) d[s] = RENORM ? 0.f : -p[s] * sum;
   for (int j = 0; j < k; ++j) {
     const int e = __builtin_amdgcn_readlane(my_e, j);
     const float v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), j));

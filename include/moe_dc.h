@@ -337,7 +337,8 @@ int moe_dispatch_backward(const void* d_rows, int32_t rows_dtype, int64_t n_toke
  *   renormalize == 0: d_logits[t, e] = sum_{j: idx_j = e} w_j * d_j - p_e * S,
  *                     p the softmax over all E logits.
  *   logits    [N, E] float32;  topk_idx, topk_w [N, k] from moe_route_topk with
- *             the same renormalize (slot 0 the largest logit)
+ *             the same renormalize; slots may have been dropped (ids outside
+ *             [0, E)) or moved since
  *   d_topk_w  [N, k] float32;  d_logits [N, E] float32, output (every element)
  * Slots whose id lies outside [0, E) add nothing.  A logit of -inf has
  * probability 0.  NaN among a row's weights (moe_route_topk writes them where
