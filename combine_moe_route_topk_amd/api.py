@@ -388,8 +388,10 @@ def moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, dst_pos: torch.Te
                          d_topk_w: Optional[torch.Tensor] = None, stream=None):
     """Gradient of moe_combine: d_out [N, D] float32/bfloat16 and the forward
     call's y [N*k, D], dst_pos, topk_w [N, k] -> (d_y [N*k, D] of y's dtype,
-    d_topk_w [N, k] float32).  Rows of d_y that no pair names (dropped pairs,
-    dst_pos outside [0, N*k)) keep what d_y held: pass a zeroed d_y then."""
+    d_topk_w [N, k] float32).  Pairs may be dropped (dst_pos outside [0, N*k)):
+    rows of d_y that no pair names are zero.  A d_y that is passed in keeps what
+    it held there, so where every pair has a row, an uninitialised one saves
+    clearing it."""
     _need(y, "y", tuple(_FLOAT_IO))
     dev = y.device
     _need(d_out, "d_out", tuple(_FLOAT_IO), dev)
@@ -404,7 +406,7 @@ def moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, dst_pos: torch.Te
         raise ValueError("y / dst_pos must hold N*k rows")
     own = []
     if d_y is None:
-        d_y = torch.empty_like(y)
+        d_y = torch.zeros_like(y)
         own.append(d_y)
     else:
         _need(d_y, "d_y", (y.dtype,), dev)
