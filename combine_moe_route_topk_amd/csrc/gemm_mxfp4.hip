@@ -84,9 +84,13 @@ __device__ Tile find_tile(int m_idx, const int32_t* __restrict__ offs, int n_exp
 }
 
 // silu(a) = a / (1 + e^-a) from the exponential and reciprocal instructions (1
-// ulp each): about 2^-21 off, beside the 2^-8 of the bf16 rounding that follows.
-// Below -87 the result is 0 (a e^a, under 2^-119, is lost with the reciprocal's
-// subnormals); -inf gives NaN, as a / (1 + e^-a) does.
+// ulp each), beside the 2^-8 of the bf16 rounding that follows.  The exponent is
+// rounded once, which a negative gate carries into the result: within 2^-21 +
+// |a| 2^-23.6, 2^-17 at a = -87.  Below -87.3 the reciprocal would be subnormal,
+// and the result is 0 in place of a e^a, under 2^-119; -inf gives NaN, as
+// a / (1 + e^-a) does.  Measured, 16384 rows over 8 experts, K 4096, F 14336: 1064
+// us; 1088 with a scaled denominator that keeps those values, 1180 with expf and
+// the division.
 __device__ __forceinline__ float silu(float a) {
   return a * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(a * -1.44269504f));
 }
