@@ -697,8 +697,9 @@ def moe_dequant_mxfp4(codes: torch.Tensor, scales: torch.Tensor,
     return out
 
 
-def _mxfp4_product(fn, rows, row_scales, index, n_index, w, w_scales, w_up, w_up_scales, y):
-    """Shared checks of the two MXFP4 products -> (device, sizes, y, own)."""
+def _mxfp4_product(fn, rows, row_scales, index, gather, w, w_scales, w_up, w_up_scales, y):
+    """Shared checks of the two MXFP4 products -> (device, sizes, y, own).
+    index: the expert of each row (gather) or the experts' offsets."""
     _mxfp4_operand(rows, row_scales, "rows", "row_scales", 2)
     dev = rows.device
     _mxfp4_operand(w, w_scales, "w", "w_scales", 3, dev)
@@ -711,7 +712,7 @@ def _mxfp4_product(fn, rows, row_scales, index, n_index, w, w_scales, w_up, w_up
     if rows.shape[1] != kh:
         raise ValueError(f"{fn}: rows have {rows.shape[1]} code bytes, w {kh}")
     _need(index, "expert_offsets / row_expert", (torch.int32,), dev)
-    if index.dim() != 1 or index.shape[0] != (e + 1 if n_index is None else n_index):
+    if index.dim() != 1 or index.shape[0] != (rows.shape[0] if gather else e + 1):
         raise ValueError(f"{fn}: expert_offsets must be [E+1], row_expert [R]")
     own = []
     if y is None:
@@ -733,7 +734,7 @@ def moe_grouped_gemm_mxfp4(rows: torch.Tensor, row_scales: torch.Tensor,
     -> y [R, N] bf16.  With w_up / w_up_scales (the shapes of w): y =
     silu(rows w) * (rows w_up).  Rows outside the offsets keep what y held."""
     dev, e, n, k, y, own = _mxfp4_product("moe_grouped_gemm_mxfp4", rows, row_scales, expert_offsets,
-                                          None, w, w_scales, w_up, w_up_scales, y)
+                                          False, w, w_scales, w_up, w_up_scales, y)
     _launch("moe_grouped_gemm_mxfp4", dev, stream,
             (_ptr(rows), _ptr(row_scales), rows.shape[0], k, _ptr(expert_offsets), e, _ptr(w),
              _ptr(w_scales), _ptr(w_up), _ptr(w_up_scales), n, _ptr(y)), own)
@@ -754,7 +755,7 @@ def moe_gather_gemm_mxfp4(rows: torch.Tensor, row_scales: torch.Tensor, row_expe
     """moe_grouped_gemm_mxfp4 over rows in any order, row r taking expert
     row_expert[r] ([R] int32; rows with an id outside [0, E) keep what y held)."""
     dev, e, n, k, y, own = _mxfp4_product("moe_gather_gemm_mxfp4", rows, row_scales, row_expert,
-                                          rows.shape[0], w, w_scales, w_up, w_up_scales, y)
+                                          True, w, w_scales, w_up, w_up_scales, y)
     if workspace is None:
         workspace = rows.new_empty(max(moe_gather_gemm_mxfp4_workspace_bytes(rows.shape[0], e), 256))
         own.append(workspace)
