@@ -711,10 +711,10 @@ __device__ __forceinline__ void tile(const uint8_t* __restrict__ rows, const uin
 // ANY: the tiles can be few, or rows be in any order (in every kernel these cost
 // SwiGLU 1% and 2% where neither is so).
 // Measured: 16384 rows over 8 experts, K 4096, F 14336 with SwiGLU, 3.85 TFLOP
-// in 1.08 ms, 3.55 PFLOP/s; K 14336, N 4096 3.66 PFLOP/s.  The card's clock
-// falls to 1.4-1.9 GHz under it; at that clock MFMAs take 55% of the cycles of
-// a long K, the rest is waiting for operands.  With all codes zero, which draws
-// less power, the same calls run 12-16% faster.
+// in 1.06 ms, 3.63 PFLOP/s; K 14336, N 4096 3.6 PFLOP/s.  The card's clock falls
+// to 1.6-1.8 GHz under it, and MFMAs take 47-48% of the cycles at that clock;
+// waves wait for 17-20% of theirs.  With all codes zero, which draws less power,
+// the same calls run 11-16% faster, without the loads into LDS 17-21%.
 template <bool GLU, int TAIL, bool FULL, bool ANY>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void tile_kernel(const uint8_t* __restrict__ rows, const uint8_t* __restrict__ row_scales, int n_rows,
@@ -780,13 +780,14 @@ GatherLayout gather_layout(int64_t n_rows, int n_experts) {
 }
 
 // Mean rows per expert from which tiles of 32 rows are taken, of 64 rows, and
-// the tile kernel.  Measured (rows per expert: times in us of 16-, 32-, 64-row
-// tiles and the tile kernel; 64 experts, K = N = 4096): 8: 104, 108, 114, -; 16:
-// 138, 120, 116, -; 32: 212, 148, 121, 128; 48: 288, 186, 138, 136; 64: 366, 225,
-// 163, 141; 128: 678, 393, 255, 166.  256 experts, K 7168, N 4096: 40 rows 847
-// and 846, 56 rows 912 and 872.  With 8 experts 32-row tiles lead up to 24: 14.7
-// against 23.4 and 16.1; 64-row tiles and the tile kernel take 17.0 and 16.7 at
-// 48, 26.3 and 16.9 at 56.
+// the tile kernel.  The rows are the call's, also those without an expert, which
+// the launch cannot know.  Measured with equally popular experts (rows per
+// expert: times in us of 16-, 32-, 64-row tiles and the tile kernel; 64 experts,
+// K = N = 4096): 8: 104, 108, 114, -; 16: 138, 120, 116, -; 32: 212, 148, 121,
+// 128; 48: 288, 186, 138, 136; 64: 366, 225, 163, 141; 128: 678, 393, 255, 166.
+// 256 experts, K 7168, N 4096: 40 rows 847 and 846, 56 rows 912 and 872.  With 8
+// experts 32-row tiles lead up to 24: 14.7 against 23.4 and 16.1; 64-row tiles
+// and the tile kernel take 17.0 and 16.7 at 48, 26.3 and 16.9 at 56.
 constexpr int64_t kNarrowRows = 10, kMiddleRows = 24, kManyRows = 48;
 
 // Row tiles at most: every expert can end in a partial one, and each holds a row.
