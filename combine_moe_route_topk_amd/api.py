@@ -732,7 +732,8 @@ def moe_grouped_gemm_mxfp4(rows: torch.Tensor, row_scales: torch.Tensor,
     """MXFP4 rows [R, K/2] with row_scales [R, K/32], grouped by expert through
     expert_offsets [E+1]; MXFP4 weights w [E, N, K/2] with w_scales [E, N, K/32]
     -> y [R, N] bf16.  With w_up / w_up_scales (the shapes of w): y =
-    silu(rows w) * (rows w_up).  Rows outside the offsets keep what y held."""
+    silu(rows w) * (rows w_up).  Rows outside the offsets keep what y held: in a
+    y that the call allocates they are uninitialised."""
     dev, e, n, k, y, own = _mxfp4_product("moe_grouped_gemm_mxfp4", rows, row_scales, expert_offsets,
                                           False, w, w_scales, w_up, w_up_scales, y)
     _launch("moe_grouped_gemm_mxfp4", dev, stream,
@@ -753,7 +754,8 @@ def moe_gather_gemm_mxfp4(rows: torch.Tensor, row_scales: torch.Tensor, row_expe
                           y: Optional[torch.Tensor] = None,
                           workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """moe_grouped_gemm_mxfp4 over rows in any order, row r taking expert
-    row_expert[r] ([R] int32; rows with an id outside [0, E) keep what y held)."""
+    row_expert[r] ([R] int32).  Rows with an id outside [0, E) keep what y held:
+    in a y that the call allocates they are uninitialised."""
     dev, e, n, k, y, own = _mxfp4_product("moe_gather_gemm_mxfp4", rows, row_scales, row_expert,
                                           True, w, w_scales, w_up, w_up_scales, y)
     if workspace is None:
