@@ -4,7 +4,9 @@ The compute lives in the HIP library ``libmoe_dc.so`` (C ABI in
 ``include/moe_dc.h``); this package is its PyTorch binding.  Importing it
 without the built library raises ImportError -- there is no CPU fallback.
 """
-from .api import (DispatchResult, MoeError, default_sort_cutoff, moe_abi_version, moe_combine,
+from .api import (BalanceLoss, DispatchResult, MoeError, default_sort_cutoff, moe_abi_version, moe_balance_loss,
+                  moe_balance_loss_backward, moe_balance_loss_workspace_bytes, moe_combine,
+                  moe_dequant_int4, moe_gather_gemm_int4, moe_gather_gemm_int4_workspace_bytes, moe_quantize_int4,
                   moe_combine_backward, moe_dequant_mxfp4, moe_dequant_rows,
                   moe_dispatch, moe_dispatch_backward, moe_dispatch_workspace_bytes, moe_gather_gemm_mxfp4,
                   moe_gather_gemm_mxfp4_workspace_bytes, moe_gather_rows,
@@ -17,7 +19,9 @@ from .api import (DispatchResult, MoeError, default_sort_cutoff, moe_abi_version
                   moe_scatter_rows)
 from ._lib import LIB_PATH, MOE_NOALLOC_SCRATCH_BYTES, MOE_SORT_AUTO, MOE_SORT_OFF, MOE_SORT_ON
 
-__all__ = ["DispatchResult", "MoeError", "default_sort_cutoff", "moe_abi_version", "moe_combine",
+__all__ = ["BalanceLoss", "moe_balance_loss", "moe_balance_loss_backward", "moe_balance_loss_workspace_bytes",
+           "moe_quantize_int4", "moe_dequant_int4", "moe_gather_gemm_int4", "moe_gather_gemm_int4_workspace_bytes",
+           "DispatchResult", "MoeError", "default_sort_cutoff", "moe_abi_version", "moe_combine",
            "moe_combine_backward", "moe_dispatch_backward", "moe_route_topk_backward",
            "moe_dequant_rows",
            "moe_dispatch", "moe_dispatch_workspace_bytes", "moe_gather_rows",

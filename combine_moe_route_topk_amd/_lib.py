@@ -63,6 +63,16 @@ SIGNATURES = {
     "moe_gather_gemm_mxfp4_workspace_bytes": (_sz, [_i64, _i32]),
     "moe_gather_gemm_mxfp4": (ctypes.c_int, [_p, _p, _i64, _i64, _p, _i32, _p, _p, _p, _p, _i64, _p,
                                              _p, _sz, _p]),
+    "moe_balance_loss_workspace_bytes": (_sz, [_i64, _i32, _i32]),
+    "moe_balance_loss": (ctypes.c_int, [_p, _p, _i64, _i32, _i32, _p, _i32, _p, _p, _p, _p, _p, _p, _p,
+                                        _sz, _p]),
+    "moe_balance_loss_backward": (ctypes.c_int, [_p, _i64, _i32, _i32, _p, _i32, _p, _p, _p, _p, _p, _p,
+                                                 _i32, _p]),
+    "moe_quantize_int4": (ctypes.c_int, [_p, _i32, _i64, _i64, _i32, _p, _p, _p, _i32, _p]),
+    "moe_dequant_int4": (ctypes.c_int, [_p, _p, _p, _i32, _i64, _i64, _i32, _p, _i32, _p]),
+    "moe_gather_gemm_int4_workspace_bytes": (_sz, [_i64, _i32]),
+    "moe_gather_gemm_int4": (ctypes.c_int, [_p, _i64, _i64, _p, _i32, _p, _p, _p, _p, _p, _p, _i32, _i32,
+                                            _i64, _p, _i32, _p, _sz, _p]),
     "moe_grouped_gemm_fp8": (ctypes.c_int, [_p, _p, _i64, _i64, _p, _i32, _p, _p, _i64, _p, _p]),
 }
 

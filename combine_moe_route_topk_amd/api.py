@@ -24,7 +24,9 @@ __all__ = ["moe_route_topk", "moe_resolve_sorted", "default_sort_cutoff", "moe_d
            "moe_grouped_swiglu", "moe_grouped_gemm_fp8", "moe_gather_swiglu_workspace_bytes",
            "moe_gather_swiglu", "moe_gather_swiglu_combine", "moe_quantize_mxfp4", "moe_dequant_mxfp4",
            "moe_grouped_gemm_mxfp4", "moe_gather_gemm_mxfp4", "moe_gather_gemm_mxfp4_workspace_bytes",
-           "moe_abi_version", "DispatchResult",
+           "moe_balance_loss", "moe_balance_loss_backward", "moe_balance_loss_workspace_bytes",
+           "moe_quantize_int4", "moe_dequant_int4", "moe_gather_gemm_int4", "moe_gather_gemm_int4_workspace_bytes",
+           "moe_abi_version", "DispatchResult", "BalanceLoss",
            "MoeError"]
 
 
@@ -767,4 +769,256 @@ def moe_gather_gemm_mxfp4(rows: torch.Tensor, row_scales: torch.Tensor, row_expe
             (_ptr(rows), _ptr(row_scales), rows.shape[0], k, _ptr(row_expert), e, _ptr(w),
              _ptr(w_scales), _ptr(w_up), _ptr(w_up_scales), n, _ptr(y), _ptr(workspace),
              workspace.numel()), own)
+    return y
+
+
+@dataclass
+class BalanceLoss:
+    loss: torch.Tensor        # [B] float32
+    z_loss: torch.Tensor      # [B] float32
+    counts: torch.Tensor      # [B, E] int32
+    probs: torch.Tensor       # [B, E] float32
+    tokens: torch.Tensor      # [B] int32
+
+
+def _balance_tokens(fn, logits, seq_offsets, token_mask):
+    """Shared checks of the balance loss and its gradient -> (device, N, E, B)."""
+    _need(logits, "logits", (torch.float32,))
+    if logits.dim() != 2:
+        raise ValueError("logits must be [N, E]")
+    dev = logits.device
+    n, e = logits.shape
+    b = 1
+    if seq_offsets is not None:
+        _need(seq_offsets, "seq_offsets", (torch.int32,), dev)
+        if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
+            raise ValueError(f"{fn}: seq_offsets must be [B + 1], B >= 1")
+        b = seq_offsets.shape[0] - 1
+    if token_mask is not None:
+        _need(token_mask, "token_mask", (torch.bool, torch.uint8), dev)
+        _shape(token_mask, "token_mask", (n,))
+    return dev, n, e, b
+
+
+@functools.lru_cache(maxsize=1024)        # a function of the sizes alone
+def moe_balance_loss_workspace_bytes(n_tokens: int, n_experts: int, n_sequences: int = 1) -> int:
+    return int(lib.moe_balance_loss_workspace_bytes(n_tokens, n_experts, n_sequences))
+
+
+def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor,
+                     seq_offsets: Optional[torch.Tensor] = None,
+                     token_mask: Optional[torch.Tensor] = None, out: Optional[BalanceLoss] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> BalanceLoss:
+    """Load-balance and z losses of a softmax top-k router with the per-expert
+    counts, per sequence: logits [N, E] float32, topk_idx [N, k] int32 (of
+    moe_route_topk), seq_offsets [B + 1] int32 (None: one sequence of all tokens),
+    token_mask [N] bool/uint8 (None: every token counts) -> BalanceLoss of
+        loss[b] = E / (k n_b) sum_e counts[b, e] probs[b, e]     (1 when even)
+        z_loss[b] = mean over b's tokens of logsumexp(logits)^2
+        counts [B, E], probs [B, E] (mean probability), tokens [B] (n_b).
+    Ids outside [0, E) are not counted.  ``out`` may carry preallocated outputs."""
+    dev, n, e, b = _balance_tokens("moe_balance_loss", logits, seq_offsets, token_mask)
+    _need(topk_idx, "topk_idx", (torch.int32,), dev)
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != n:
+        raise ValueError(f"topk_idx must be [N={n}, k]")
+    own = []
+    if out is None:
+        out = BalanceLoss(logits.new_empty(b), logits.new_empty(b), topk_idx.new_empty((b, e)),
+                          logits.new_empty((b, e)), topk_idx.new_empty(b))
+        own += [out.loss, out.z_loss, out.counts, out.probs, out.tokens]
+    else:
+        for name, dtype, shape in (("loss", torch.float32, (b,)), ("z_loss", torch.float32, (b,)),
+                                   ("counts", torch.int32, (b, e)), ("probs", torch.float32, (b, e)),
+                                   ("tokens", torch.int32, (b,))):
+            _need(getattr(out, name), f"out.{name}", (dtype,), dev)
+            _shape(getattr(out, name), f"out.{name}", shape)
+    if workspace is None:
+        workspace = logits.new_empty(max(moe_balance_loss_workspace_bytes(n, e, b), 256), dtype=torch.uint8)
+        own.append(workspace)
+    else:
+        _need(workspace, "workspace", (torch.uint8,), dev)
+    _launch("moe_balance_loss", dev, stream,
+            (_ptr(logits), _ptr(topk_idx), n, e, topk_idx.shape[1], _ptr(seq_offsets), b,
+             _ptr(token_mask), _ptr(out.loss), _ptr(out.z_loss), _ptr(out.counts), _ptr(out.probs),
+             _ptr(out.tokens), _ptr(workspace), workspace.numel()), own)
+    return out
+
+
+def moe_balance_loss_backward(logits: torch.Tensor, counts: torch.Tensor, tokens: torch.Tensor, k: int,
+                              d_loss: torch.Tensor, d_z_loss: Optional[torch.Tensor] = None,
+                              seq_offsets: Optional[torch.Tensor] = None,
+                              token_mask: Optional[torch.Tensor] = None,
+                              d_logits: Optional[torch.Tensor] = None, accumulate: bool = False,
+                              stream=None) -> torch.Tensor:
+    """Gradient of moe_balance_loss: its logits, seq_offsets and token_mask, the
+    counts [B, E] and tokens [B] that it returned (or their sums over the ranks
+    that share a batch), k ids per token, d_loss [B] and d_z_loss [B] (None: 0)
+    -> d_logits [N, E] float32, zero for tokens that do not count.  With
+    accumulate the gradient is added to d_logits, which has to be given."""
+    dev, n, e, b = _balance_tokens("moe_balance_loss_backward", logits, seq_offsets, token_mask)
+    for name, t, dtype, shape in (("counts", counts, torch.int32, (b, e)), ("tokens", tokens, torch.int32, (b,)),
+                                  ("d_loss", d_loss, torch.float32, (b,))):
+        _need(t, name, (dtype,), dev)
+        _shape(t, name, shape)
+    if d_z_loss is not None:
+        _need(d_z_loss, "d_z_loss", (torch.float32,), dev)
+        _shape(d_z_loss, "d_z_loss", (b,))
+    own = []
+    if d_logits is None:
+        if accumulate:
+            raise ValueError("accumulate needs d_logits")
+        d_logits = torch.empty_like(logits)
+        own.append(d_logits)
+    else:
+        _need(d_logits, "d_logits", (torch.float32,), dev)
+        _shape(d_logits, "d_logits", (n, e))
+    _launch("moe_balance_loss_backward", dev, stream,
+            (_ptr(logits), n, e, k, _ptr(seq_offsets), b, _ptr(token_mask), _ptr(counts), _ptr(tokens),
+             _ptr(d_loss), _ptr(d_z_loss), _ptr(d_logits), int(bool(accumulate))), own)
+    return d_logits
+
+
+def _int4_operand(codes, scales, biases, name: str, scales_name: str, biases_name: str, dims: int, dev=None) -> int:
+    """Checks codes [..., K/2], scales [..., K/group] and biases -> the group."""
+    _need(codes, name, (torch.uint8,), dev)
+    _need(scales, scales_name, tuple(_FLOAT_IO), codes.device)
+    cs, ss = codes.shape, scales.shape
+    if len(cs) != dims or len(ss) != dims or ss[:-1] != cs[:-1] or cs[-1] == 0 or ss[-1] == 0:
+        raise ValueError(f"{name} and {scales_name} must be [..., K/2] and [..., K/group] of {dims} "
+                         f"dimensions, got {tuple(cs)} and {tuple(ss)}")
+    group, rest = divmod(2 * cs[-1], ss[-1])
+    if rest or group not in (32, 64, 128):
+        raise ValueError(f"{scales_name} has {ss[-1]} scales for {2 * cs[-1]} elements: "
+                         "groups must hold 32, 64 or 128")
+    if biases is not None:
+        _need(biases, biases_name, (scales.dtype,), codes.device)
+        _shape(biases, biases_name, ss)
+    return group
+
+
+def moe_quantize_int4(x: torch.Tensor, group: int = 128, affine: bool = False,
+                      scale_dtype: torch.dtype = torch.bfloat16, codes: Optional[torch.Tensor] = None,
+                      scales: Optional[torch.Tensor] = None, biases: Optional[torch.Tensor] = None,
+                      stream=None):
+    """x [R, K] float32/bfloat16 -> 4-bit integer (codes [R, K/2] uint8, two per
+    byte, even element low; scales [R, K/group] of scale_dtype; biases [R, K/group]
+    with affine, else None): x ~ scale * (code - 8), or scale * code + bias.
+    group 32, 64 or 128.  Weights [E, N, K] are quantised as x.view(E * N, K).
+    Outputs that are passed in name the form: scales its type, biases the affine
+    one."""
+    _need(x, "x", tuple(_FLOAT_IO))
+    dev = x.device
+    if group not in (32, 64, 128):
+        raise ValueError(f"group is {group}, expected 32, 64 or 128")
+    if x.dim() != 2 or x.shape[1] == 0 or x.shape[1] % group:
+        raise ValueError(f"x must be [R, K] with K % {group} == 0")
+    r, k = x.shape
+    own = []
+    if codes is None:
+        codes = x.new_empty((r, k // 2), dtype=torch.uint8)
+        own.append(codes)
+    else:
+        _need(codes, "codes", (torch.uint8,), dev)
+        _shape(codes, "codes", (r, k // 2))
+    if scales is None:
+        if scale_dtype not in _FLOAT_IO:
+            raise TypeError(f"scale_dtype is {scale_dtype}, expected one of {tuple(_FLOAT_IO)}")
+        scales = x.new_empty((r, k // group), dtype=scale_dtype)
+        own.append(scales)
+    else:
+        _need(scales, "scales", tuple(_FLOAT_IO), dev)
+        _shape(scales, "scales", (r, k // group))
+    if biases is not None:
+        _need(biases, "biases", (scales.dtype,), dev)
+        _shape(biases, "biases", (r, k // group))
+    elif affine:
+        biases = torch.empty_like(scales)
+        own.append(biases)
+    _launch("moe_quantize_int4", dev, stream,
+            (_ptr(x), _FLOAT_IO[x.dtype], r, k, group, _ptr(codes), _ptr(scales), _ptr(biases),
+             _FLOAT_IO[scales.dtype]), own)
+    return codes, scales, biases
+
+
+def moe_dequant_int4(codes: torch.Tensor, scales: torch.Tensor, biases: Optional[torch.Tensor] = None,
+                     out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """4-bit integer codes [R, K/2] with scales (and biases) [R, K/group] -> their
+    values [R, K]."""
+    group = _int4_operand(codes, scales, biases, "codes", "scales", "biases", 2)
+    dev = codes.device
+    r, k = codes.shape[0], codes.shape[1] * 2
+    own = []
+    if out is None:
+        if out_dtype not in _FLOAT_IO:
+            raise TypeError(f"out_dtype is {out_dtype}, expected one of {tuple(_FLOAT_IO)}")
+        out = codes.new_empty((r, k), dtype=out_dtype)
+        own.append(out)
+    else:
+        _need(out, "out", tuple(_FLOAT_IO), dev)
+        _shape(out, "out", (r, k))
+    _launch("moe_dequant_int4", dev, stream,
+            (_ptr(codes), _ptr(scales), _ptr(biases), _FLOAT_IO[scales.dtype], r, k, group, _ptr(out),
+             _FLOAT_IO[out.dtype]), own)
+    return out
+
+
+@functools.lru_cache(maxsize=1024)        # a function of the sizes alone
+def moe_gather_gemm_int4_workspace_bytes(n_rows: int, n_experts: int) -> int:
+    return int(lib.moe_gather_gemm_int4_workspace_bytes(n_rows, n_experts))
+
+
+def moe_gather_gemm_int4(rows: torch.Tensor, row_expert: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                         w_biases: Optional[torch.Tensor] = None, w_up: Optional[torch.Tensor] = None,
+                         w_up_scales: Optional[torch.Tensor] = None,
+                         w_up_biases: Optional[torch.Tensor] = None,
+                         out_dtype: torch.dtype = torch.bfloat16, y: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Products of bf16 rows [R, K] in any order with their experts' 4-bit integer
+    weights, row r taking expert row_expert[r] ([R] int32): w [E, N, K/2] codes
+    with w_scales (and w_biases) [E, N, K/group] float32/bfloat16 -> y [R, N] of
+    out_dtype (float32/bfloat16).  With w_up (the shapes of w): y = silu(rows w) *
+    (rows w_up).  One expert and zeros in row_expert make a dense product.  Rows
+    with an id outside [0, E) keep what y held: in a y that the call allocates they
+    are uninitialised."""
+    fn = "moe_gather_gemm_int4"
+    _need(rows, "rows", (torch.bfloat16,))
+    dev = rows.device
+    group = _int4_operand(w, w_scales, w_biases, "w", "w_scales", "w_biases", 3, dev)
+    if (w_up is None) != (w_up_scales is None):
+        raise ValueError(f"{fn}: w_up and w_up_scales go together")
+    if w_up is not None:
+        _int4_operand(w_up, w_up_scales, w_up_biases, "w_up", "w_up_scales", "w_up_biases", 3, dev)
+        _shape(w_up, "w_up", w.shape)
+        _shape(w_up_scales, "w_up_scales", w_scales.shape)
+        if w_up_scales.dtype != w_scales.dtype:
+            raise TypeError(f"w_up_scales has dtype {w_up_scales.dtype}, w_scales {w_scales.dtype}")
+    if (w_up is not None or w_up_biases is not None) and (w_up_biases is None) != (w_biases is None):
+        raise ValueError(f"{fn}: w_biases and w_up_biases go together")
+    if w_up is None and w_up_biases is not None:
+        raise ValueError(f"{fn}: w_up_biases without w_up")
+    e, n, kh = w.shape
+    if rows.dim() != 2 or rows.shape[1] != 2 * kh:
+        raise ValueError(f"{fn}: rows must be [R, {2 * kh}]")
+    r = rows.shape[0]
+    _need(row_expert, "row_expert", (torch.int32,), dev)
+    _shape(row_expert, "row_expert", (r,))
+    own = []
+    if y is None:
+        if out_dtype not in _FLOAT_IO:
+            raise TypeError(f"out_dtype is {out_dtype}, expected one of {tuple(_FLOAT_IO)}")
+        y = rows.new_empty((r, n), dtype=out_dtype)
+        own.append(y)
+    else:
+        _need(y, "y", tuple(_FLOAT_IO), dev)
+        _shape(y, "y", (r, n))
+    if workspace is None:
+        workspace = rows.new_empty(max(moe_gather_gemm_int4_workspace_bytes(r, e), 256), dtype=torch.uint8)
+        own.append(workspace)
+    else:
+        _need(workspace, "workspace", (torch.uint8,), dev)
+    _launch(fn, dev, stream,
+            (_ptr(rows), r, 2 * kh, _ptr(row_expert), e, _ptr(w), _ptr(w_scales), _ptr(w_biases), _ptr(w_up),
+             _ptr(w_up_scales), _ptr(w_up_biases), _FLOAT_IO[w_scales.dtype], group, n, _ptr(y),
+             _FLOAT_IO[y.dtype], _ptr(workspace), workspace.numel()), own)
     return y

@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe_dc.so")
 SOURCES = ["api.cpp", "route_topk.hip", "dispatch.hip", "combine.hip", "grouped_swiglu.hip",
            "grouped_gemm_fp8.hip", "gather_swiglu.hip", "backward.hip", "mxfp4.hip",
-           "gemm_mxfp4.hip"]
+           "gemm_mxfp4.hip", "balance.hip", "int4.hip", "gemm_int4.hip"]
 ARCH = "gfx950"
 
 

@@ -722,4 +722,162 @@ int moe_gather_gemm_mxfp4(const uint8_t* rows, const uint8_t* row_scales, int64_
                     fn);
 }
 
+size_t moe_balance_loss_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t n_sequences) {
+  if (n_tokens < 0 || n_tokens > INT32_MAX || n_experts < 1 || n_experts > MOE_MAX_EXPERTS ||
+      n_sequences < 1 || n_sequences > MOE_MAX_SEQUENCES)
+    return 0;
+  return moe::balance_workspace_bytes(n_tokens, n_experts, n_sequences);
+}
+
+namespace {
+int check_balance(const char* fn, int64_t n_tokens, int32_t n_experts, int32_t k,
+                  const int32_t* seq_offsets, int32_t n_sequences) {
+  const int rc = check_routing_sizes(fn, n_tokens, n_experts, k);
+  if (rc) return rc;
+  if (n_sequences < 1) return fail(MOE_ERR_ARG, "%s: n_sequences < 1", fn);
+  if (n_sequences > MOE_MAX_SEQUENCES)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: n_sequences > %d", fn, MOE_MAX_SEQUENCES);
+  if (!seq_offsets && n_sequences != 1)
+    return fail(MOE_ERR_ARG, "%s: %d sequences need seq_offsets", fn, n_sequences);
+  return MOE_OK;
+}
+}  // namespace
+
+int moe_balance_loss(const float* logits, const int32_t* topk_idx, int64_t n_tokens,
+                     int32_t n_experts, int32_t k, const int32_t* seq_offsets, int32_t n_sequences,
+                     const uint8_t* token_mask, float* loss, float* z_loss, int32_t* counts,
+                     float* probs, int32_t* tokens, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  const char* fn = "moe_balance_loss";
+  const int rc = check_balance(fn, n_tokens, n_experts, k, seq_offsets, n_sequences);
+  if (rc) return rc;
+  if (((!logits || !topk_idx) && n_tokens > 0) || !loss || !z_loss || !counts || !probs || !tokens)
+    return fail(MOE_ERR_ARG, "%s: null pointer argument", fn);
+  if (off(logits, 4) || off(topk_idx, 4) || off(seq_offsets, 4) || off(loss, 4) || off(z_loss, 4) ||
+      off(counts, 4) || off(probs, 4) || off(tokens, 4))
+    return fail(MOE_ERR_ARG, "%s: pointers must be aligned to their elements", fn);
+  const size_t need = moe::balance_workspace_bytes(n_tokens, n_experts, n_sequences);
+  if (!workspace || workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                workspace ? workspace_bytes : size_t(0));
+  if (off(workspace, 256))
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace must be 256-byte aligned", fn);
+  const moe::BalanceForward g{logits, topk_idx, n_tokens, n_experts, k, seq_offsets, n_sequences,
+                              token_mask, loss, z_loss, counts, probs, tokens};
+  return hip_status(moe::launch_balance_loss(g, workspace, static_cast<hipStream_t>(stream)), fn);
+}
+
+int moe_balance_loss_backward(const float* logits, int64_t n_tokens, int32_t n_experts, int32_t k,
+                              const int32_t* seq_offsets, int32_t n_sequences,
+                              const uint8_t* token_mask, const int32_t* counts,
+                              const int32_t* tokens, const float* d_loss, const float* d_z_loss,
+                              float* d_logits, int32_t accumulate, void* stream) {
+  const char* fn = "moe_balance_loss_backward";
+  const int rc = check_balance(fn, n_tokens, n_experts, k, seq_offsets, n_sequences);
+  if (rc) return rc;
+  if (n_tokens == 0) return ok();
+  if (!logits || !counts || !tokens || !d_loss || !d_logits)
+    return fail(MOE_ERR_ARG, "%s: null pointer argument", fn);
+  if (off(logits, 4) || off(seq_offsets, 4) || off(counts, 4) || off(tokens, 4) || off(d_loss, 4) ||
+      off(d_z_loss, 4) || off(d_logits, 4))
+    return fail(MOE_ERR_ARG, "%s: pointers must be aligned to their elements", fn);
+  const moe::BalanceBackward g{logits, n_tokens, n_experts, k, seq_offsets, n_sequences, token_mask,
+                               counts, tokens, d_loss, d_z_loss, d_logits, accumulate ? 1 : 0};
+  return hip_status(moe::launch_balance_loss_backward(g, static_cast<hipStream_t>(stream)), fn);
+}
+
+namespace {
+bool float_type(int32_t dtype) { return dtype == MOE_F32 || dtype == MOE_BF16; }
+
+int check_int4_rows(const char* fn, int32_t dtype, int32_t scale_dtype, int64_t n_rows, int64_t k_dim,
+                    int32_t group) {
+  if (n_rows < 0) return fail(MOE_ERR_ARG, "%s: n_rows < 0", fn);
+  if (k_dim < 1) return fail(MOE_ERR_ARG, "%s: k_dim < 1", fn);
+  if (!float_type(dtype) || !float_type(scale_dtype))
+    return fail(MOE_ERR_ARG, "%s: types must be MOE_F32 or MOE_BF16", fn);
+  if (group != 32 && group != 64 && group != 128)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: group must be 32, 64 or 128 (got %d)", fn, group);
+  if (k_dim % group != 0) return fail(MOE_ERR_UNSUPPORTED, "%s: k_dim must be a multiple of the group", fn);
+  if (n_rows > (int64_t(1) << 40) / k_dim)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^40 elements", fn);
+  return MOE_OK;
+}
+}  // namespace
+
+int moe_quantize_int4(const void* x, int32_t x_dtype, int64_t n_rows, int64_t k_dim, int32_t group,
+                      uint8_t* codes, void* scales, void* biases, int32_t scale_dtype, void* stream) {
+  const char* fn = "moe_quantize_int4";
+  const int rc = check_int4_rows(fn, x_dtype, scale_dtype, n_rows, k_dim, group);
+  if (rc) return rc;
+  if (n_rows == 0) return ok();
+  if (!x || !codes || !scales) return fail(MOE_ERR_ARG, "%s: null pointer argument", fn);
+  if (off(x, 16) || off(codes, 4) || off(scales, 4) || off(biases, 4))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: x must be 16-byte, codes, scales and biases 4-byte aligned", fn);
+  return hip_status(moe::launch_quantize_int4(x, x_dtype == MOE_BF16, n_rows * k_dim, group, codes, scales,
+                                              biases, scale_dtype == MOE_BF16,
+                                              static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+int moe_dequant_int4(const uint8_t* codes, const void* scales, const void* biases, int32_t scale_dtype,
+                     int64_t n_rows, int64_t k_dim, int32_t group, void* out, int32_t out_dtype,
+                     void* stream) {
+  const char* fn = "moe_dequant_int4";
+  const int rc = check_int4_rows(fn, out_dtype, scale_dtype, n_rows, k_dim, group);
+  if (rc) return rc;
+  if (n_rows == 0) return ok();
+  if (!codes || !scales || !out) return fail(MOE_ERR_ARG, "%s: null pointer argument", fn);
+  if (off(out, 16) || off(codes, 4) || off(scales, 4) || off(biases, 4))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: out must be 16-byte, codes, scales and biases 4-byte aligned", fn);
+  return hip_status(moe::launch_dequant_int4(codes, scales, biases, scale_dtype == MOE_BF16, n_rows * k_dim,
+                                             group, out, out_dtype == MOE_BF16,
+                                             static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+size_t moe_gather_gemm_int4_workspace_bytes(int64_t n_rows, int32_t n_experts) {
+  if (n_rows < 0 || n_rows > INT32_MAX || n_experts < 1 || n_experts > MOE_MAX_EXPERTS) return 0;
+  return moe::gather_gemm_int4_workspace_bytes(n_rows, n_experts);
+}
+
+int moe_gather_gemm_int4(const void* rows, int64_t n_rows, int64_t k_dim, const int32_t* row_expert,
+                         int32_t n_experts, const uint8_t* w, const void* w_scales,
+                         const void* w_biases, const uint8_t* w_up, const void* w_up_scales,
+                         const void* w_up_biases, int32_t scale_dtype, int32_t group, int64_t n_dim,
+                         void* y, int32_t y_dtype, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  const char* fn = "moe_gather_gemm_int4";
+  if (n_rows < 0) return fail(MOE_ERR_ARG, "%s: n_rows < 0", fn);
+  if (k_dim < 1 || n_dim < 1 || n_experts < 1) return fail(MOE_ERR_ARG, "%s: sizes must be >= 1", fn);
+  if (!float_type(scale_dtype) || !float_type(y_dtype))
+    return fail(MOE_ERR_ARG, "%s: scale and output types must be MOE_F32 or MOE_BF16", fn);
+  if (!w_up != !w_up_scales) return fail(MOE_ERR_ARG, "%s: w_up and w_up_scales go together", fn);
+  if (w_up ? !w_biases != !w_up_biases : w_up_biases != nullptr)
+    return fail(MOE_ERR_ARG, "%s: w_biases and w_up_biases go together", fn);
+  if (n_experts > MOE_MAX_EXPERTS) return fail(MOE_ERR_UNSUPPORTED, "%s: n_experts > %d", fn, MOE_MAX_EXPERTS);
+  if (group != 32 && group != 64 && group != 128)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: group must be 32, 64 or 128 (got %d)", fn, group);
+  if (k_dim % group != 0) return fail(MOE_ERR_UNSUPPORTED, "%s: k_dim must be a multiple of the group", fn);
+  if (k_dim > (int64_t(1) << 22) || n_dim > (int64_t(1) << 22))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: k_dim and n_dim must be at most %d", fn, 1 << 22);
+  if (n_rows > INT32_MAX) return fail(MOE_ERR_UNSUPPORTED, "%s: n_rows exceeds the int32 range", fn);
+  const moe::Int4Product g{rows, n_rows, k_dim, n_experts, w, w_scales, w_biases, w_up, w_up_scales, w_up_biases,
+                           scale_dtype == MOE_BF16, group, n_dim, y, y_dtype == MOE_BF16};
+  if (n_rows > 0 && moe::gemm_int4_blocks(g) > moe::kMaxInt4Blocks)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: too many tiles", fn);
+  if (n_rows == 0) return ok();
+  if (!rows || !row_expert || !w || !w_scales || !y) return fail(MOE_ERR_ARG, "%s: null pointer argument", fn);
+  if (off(rows, 16) || off(w, 16) || off(w_up, 16) || off(y, 16))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: rows, weights and y must be 16-byte aligned", fn);
+  if (off(w_scales, 4) || off(w_biases, 4) || off(w_up_scales, 4) || off(w_up_biases, 4) || off(row_expert, 4))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: scales, biases and indices must be 4-byte aligned", fn);
+  const size_t need = moe::gather_gemm_int4_workspace_bytes(n_rows, n_experts);
+  if (!workspace || workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                workspace ? workspace_bytes : size_t(0));
+  if (off(workspace, 256))
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace must be 256-byte aligned", fn);
+  return hip_status(moe::launch_gather_gemm_int4(g, row_expert, workspace, static_cast<hipStream_t>(stream)), fn);
+}
+
 }  // extern "C"

@@ -180,4 +180,62 @@ size_t gather_gemm_mxfp4_workspace_bytes(int64_t n_rows, int n_experts);
 hipError_t launch_gather_gemm_mxfp4(const Mxfp4Product& g, const int32_t* row_expert,
                                     void* workspace, hipStream_t stream);
 
+// ---- balance and z losses of the router
+struct BalanceForward {
+  const float* logits;
+  const int32_t* topk_idx;
+  int64_t n_tokens;
+  int n_experts, k;
+  const int32_t* seq_offsets;    // null: one sequence of all tokens
+  int n_seqs;
+  const uint8_t* token_mask;     // null: every token counts
+  float *loss, *z_loss;
+  int32_t* counts;
+  float* probs;
+  int32_t* tokens;
+};
+size_t balance_workspace_bytes(int64_t n_tokens, int n_experts, int64_t n_seqs);
+hipError_t launch_balance_loss(const BalanceForward& g, void* workspace, hipStream_t stream);
+
+struct BalanceBackward {
+  const float* logits;
+  int64_t n_tokens;
+  int n_experts, k;
+  const int32_t* seq_offsets;
+  int n_seqs;
+  const uint8_t* token_mask;
+  const int32_t* counts;
+  const int32_t* tokens;
+  const float *d_loss, *d_z_loss;
+  float* d_logits;
+  int accumulate;
+};
+hipError_t launch_balance_loss_backward(const BalanceBackward& g, hipStream_t stream);
+
+// ---- 4-bit integer weights, one scale (and bias) per group of 32, 64 or 128
+hipError_t launch_quantize_int4(const void* x, int x_bf16, int64_t n_elems, int group, void* codes,
+                                void* scales, void* biases, int scales_bf16, hipStream_t stream);
+hipError_t launch_dequant_int4(const void* codes, const void* scales, const void* biases, int scales_bf16,
+                               int64_t n_elems, int group, void* out, int out_bf16, hipStream_t stream);
+
+// Operands of an expert product; w_up null: no SwiGLU; biases null: symmetric.
+struct Int4Product {
+  const void* rows;
+  int64_t n_rows, k_dim;
+  int n_experts;
+  const void *w, *w_scales, *w_biases;
+  const void *w_up, *w_up_scales, *w_up_biases;
+  int scales_bf16, group;
+  int64_t n_dim;
+  void* y;
+  int y_bf16;
+};
+// Workgroups of the product's launch, of which one launch takes kMaxInt4Blocks
+// (256 threads each).
+constexpr int64_t kMaxInt4Blocks = (int64_t(1) << 24) - 1;
+int64_t gemm_int4_blocks(const Int4Product& g);
+size_t gather_gemm_int4_workspace_bytes(int64_t n_rows, int n_experts);
+hipError_t launch_gather_gemm_int4(const Int4Product& g, const int32_t* row_expert, void* workspace,
+                                   hipStream_t stream);
+
 }  // namespace moe

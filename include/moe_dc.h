@@ -86,6 +86,7 @@ enum { MOE_SORT_AUTO = -1, MOE_SORT_OFF = 0, MOE_SORT_ON = 1 };
 /* Limits of this implementation. */
 #define MOE_MAX_EXPERTS 1024
 #define MOE_MAX_TOPK 64
+#define MOE_MAX_SEQUENCES (1 << 20)
 
 /* ABI version (MOE_DC_ABI_VERSION of the built library). */
 int moe_abi_version(void);
@@ -566,6 +567,133 @@ int moe_gather_gemm_mxfp4(const uint8_t* rows, const uint8_t* row_scales, int64_
                           const uint8_t* w, const uint8_t* w_scales, const uint8_t* w_up,
                           const uint8_t* w_up_scales, int64_t n_dim, void* y, void* workspace,
                           size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- balance
+ * Auxiliary losses of a softmax top-k router, for each sequence of tokens, and
+ * the per-expert counts they rest on.  Sequence b holds the tokens
+ * [seq_offsets[b], seq_offsets[b+1]); of these a token counts if its mask byte
+ * is not 0 and some logit of it is above -inf (or NaN).  With p_t the softmax of
+ * token t's E logits and n_b the counted tokens of b:
+ *   counts[b, e] = #{(t, j) : t counts, topk_idx[t, j] = e}
+ *   probs[b, e]  = sum_t p[t, e] / n_b
+ *   loss[b]      = E / (k n_b) * sum_e counts[b, e] probs[b, e]
+ *   z_loss[b]    = sum_t (log sum_e exp(logits[t, e]))^2 / n_b
+ * loss is 1 where tokens and probabilities are spread evenly, up to E where all
+ * go to one expert.  All four are 0 where n_b = 0.  Ids outside [0, E) (dropped
+ * slots) are not counted; the same id twice counts twice.  A logit of -inf (a
+ * masked expert) has probability 0.  A NaN or +inf logit of a counted token makes
+ * probs, loss and z_loss of its sequence NaN.
+ * fp32 sums in a fixed order: the same inputs give the same bits.
+ *
+ * moe_balance_loss_workspace_bytes -- workspace of moe_balance_loss; 0 for
+ * invalid sizes. */
+size_t moe_balance_loss_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t n_sequences);
+
+/* moe_balance_loss
+ *   logits       [N, E] float32;  topk_idx [N, k] int32 (moe_route_topk's)
+ *   seq_offsets  [n_sequences + 1] int32, device-resident, non-decreasing, or
+ *                null with n_sequences = 1: all tokens
+ *   token_mask   [N] bytes, or null: every token counts
+ *   loss, z_loss [n_sequences] float32;  counts [n_sequences, E] int32;
+ *   probs [n_sequences, E] float32;  tokens [n_sequences] int32 (n_b): outputs
+ *   workspace    moe_balance_loss_workspace_bytes(N, E, n_sequences) bytes,
+ *                256-byte aligned, clobbered
+ * N == 0 writes zeros.  Errors: those of moe_route_topk (k is the number of ids
+ * per token), with MOE_ERR_ARG for n_sequences < 1, more than one sequence
+ * without offsets or misaligned pointers, MOE_ERR_UNSUPPORTED for n_sequences >
+ * MOE_MAX_SEQUENCES; MOE_ERR_WORKSPACE for a short or misaligned workspace. */
+int moe_balance_loss(const float* logits, const int32_t* topk_idx, int64_t n_tokens,
+                     int32_t n_experts, int32_t k, const int32_t* seq_offsets, int32_t n_sequences,
+                     const uint8_t* token_mask, float* loss, float* z_loss, int32_t* counts,
+                     float* probs, int32_t* tokens, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/* moe_balance_loss_backward -- gradient of the two losses with respect to the
+ * logits, the counts standing for constants (the selection has no gradient):
+ *   d_logits[t, e] = p[t, e] (u_e - sum_i p[t, i] u_i + 2 d_z_loss[b] lse_t / n_b),
+ *   u_e = d_loss[b] (E counts[b, e] - k n_b) / (k n_b^2)
+ * for the counted tokens of sequence b, 0 for all others.  logits, seq_offsets,
+ * token_mask and k are those of the forward call, counts and tokens its outputs,
+ * or their sums over ranks that share the batch: then d_logits is the gradient of
+ * the loss of the whole batch.
+ *   d_loss    [n_sequences] float32;  d_z_loss [n_sequences] float32, or null: 0
+ *   d_logits  [N, E] float32, output (every element); with accumulate != 0 the
+ *             gradient is added to what it holds (moe_route_topk_backward's)
+ * Errors: those of moe_balance_loss; N == 0 is a no-op. */
+int moe_balance_loss_backward(const float* logits, int64_t n_tokens, int32_t n_experts, int32_t k,
+                              const int32_t* seq_offsets, int32_t n_sequences,
+                              const uint8_t* token_mask, const int32_t* counts,
+                              const int32_t* tokens, const float* d_loss, const float* d_z_loss,
+                              float* d_logits, int32_t accumulate, void* stream);
+
+/* ---------------------------------------------------------------- 4-bit integers
+ * Weights as 4-bit integers q = 0 .. 15 with one scale s, and in the affine form
+ * one bias b, per group of 32, 64 or 128 consecutive elements of a row ([ET-PR]:
+ * the quantised gather of the affine mode):
+ *   w = s (q - 8)   (biases null),      w = s q + b.
+ * Two codes share a byte, the even element in the low nibble: a row of K elements
+ * is K/2 code bytes and K/group scales (biases) of one type, float32 or bfloat16.
+ *
+ * moe_quantize_int4 -- with T the rounding to the scales' type, the difference,
+ * the constants 1/7 and 1/15 and the products with them in fp32, and the quotients
+ * rounded as exact numbers, ties to even:
+ *   symmetric:  s = T(max |x| * (1/7)),                     q = clamp(rne(x / s) + 8, 0, 15)
+ *   affine:     s = T((max x - min x) * (1/15)), b = T(min x), q = clamp(rne((x - b) / s), 0, 15)
+ * s = 0 (all zero or too small, or in the affine form all equal) gives q = 8, or
+ * q = 0.  A group that holds a NaN or an infinity, or whose max - min or rounded
+ * bias is infinite, gets s (and b) = NaN.
+ *   x [n_rows, K] of x_dtype (MOE_F32 or MOE_BF16), 16-byte aligned
+ *   codes [n_rows, K/2] uint8, scales and biases [n_rows, K/group] of scale_dtype
+ *   (MOE_F32 or MOE_BF16), outputs, 4-byte aligned; biases null: symmetric
+ * Errors: MOE_ERR_ARG for null pointers (unless n_rows == 0), n_rows < 0, K < 1
+ * or another type; MOE_ERR_UNSUPPORTED for another group, K % group != 0,
+ * misaligned pointers or more than 2^40 elements. */
+int moe_quantize_int4(const void* x, int32_t x_dtype, int64_t n_rows, int64_t k_dim, int32_t group,
+                      uint8_t* codes, void* scales, void* biases, int32_t scale_dtype, void* stream);
+
+/* moe_dequant_int4 -- the values: s (q - 8), or s q + b in one fused step, in
+ * fp32, rounded to out_dtype (MOE_F32 or MOE_BF16).  out [n_rows, K], 16-byte
+ * aligned.  Errors: those of moe_quantize_int4. */
+int moe_dequant_int4(const uint8_t* codes, const void* scales, const void* biases, int32_t scale_dtype,
+                     int64_t n_rows, int64_t k_dim, int32_t group, void* out, int32_t out_dtype,
+                     void* stream);
+
+/* moe_gather_gemm_int4_workspace_bytes -- workspace of moe_gather_gemm_int4.
+ * 0 for invalid sizes. */
+size_t moe_gather_gemm_int4_workspace_bytes(int64_t n_rows, int32_t n_experts);
+
+/* moe_gather_gemm_int4 -- expert products with 4-bit integer weights over bf16
+ * rows in any order, row r taking expert e = row_expert[r] (the unsorted dispatch,
+ * or with one expert a dense matrix):
+ *   g[r, n] = sum_k rows[r, k] w[e, n, k]
+ *   y[r, n] = g[r, n]                          w_up null
+ *   y[r, n] = silu(g[r, n]) * u[r, n]          u: g with w_up
+ * rounded to y_dtype once.  Codes are multiplied exactly, a group's sum and the
+ * sum over groups are fp32, in a fixed order.  silu as in moe_grouped_gemm_mxfp4
+ * for a bf16 y, by the accurate exponential and a division for fp32.  A NaN scale
+ * or bias makes its column's outputs NaN; a NaN or an infinity in a row makes the
+ * row's outputs of g NaN or infinite, and no other row's.  Rows whose id lies
+ * outside [0, E) leave y as it was.
+ *   rows        [n_rows, K] bfloat16, 16-byte aligned
+ *   row_expert  [n_rows] int32, device-resident
+ *   w, w_up     [E, N, K/2] codes, 16-byte aligned; w_up may be null
+ *   w_scales, w_biases, w_up_scales, w_up_biases  [E, N, K/group] of scale_dtype,
+ *               4-byte aligned; the biases null for symmetric weights
+ *   y           [n_rows, N] of y_dtype (MOE_F32 or MOE_BF16), output, 16-byte aligned
+ *   workspace   moe_gather_gemm_int4_workspace_bytes(n_rows, E) bytes, 256-byte
+ *               aligned, clobbered
+ * Errors: MOE_ERR_ARG for null pointers (unless n_rows == 0), n_rows < 0, sizes
+ * < 1, other types, or w_up without its scales, or biases for one of w and w_up
+ * only; MOE_ERR_UNSUPPORTED for another group than 32, 64 or 128, K % group != 0,
+ * K or N above 2^22, E > MOE_MAX_EXPERTS, n_rows beyond the int32 range, too many
+ * tiles or misaligned pointers; MOE_ERR_WORKSPACE for a short or misaligned
+ * workspace. */
+int moe_gather_gemm_int4(const void* rows, int64_t n_rows, int64_t k_dim, const int32_t* row_expert,
+                         int32_t n_experts, const uint8_t* w, const void* w_scales,
+                         const void* w_biases, const uint8_t* w_up, const void* w_up_scales,
+                         const void* w_up_biases, int32_t scale_dtype, int32_t group, int64_t n_dim,
+                         void* y, int32_t y_dtype, void* workspace, size_t workspace_bytes,
+                         void* stream);
 
 #ifdef __cplusplus
 }
