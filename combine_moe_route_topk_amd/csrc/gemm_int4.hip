@@ -26,9 +26,8 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kWaves = 4;              // of a workgroup, each a quarter of K
-constexpr int kT = 4;                  // 16-column tiles of a wave: 64 columns
 constexpr int kStep = 128;             // elements of K that one 16-byte load per lane covers
+constexpr int kUnit = 256;             // elements of K asked for together: whole lines of a weight row
 
 struct Product {
   const uint16_t* rows;
@@ -58,32 +57,64 @@ __device__ __forceinline__ bf16x8 evens_odds(u32x4 v) {
   return __builtin_bit_cast(bf16x8, u32x4{__builtin_amdgcn_perm(v.y, v.x, 0x05040100u), __builtin_amdgcn_perm(v.w, v.z, 0x05040100u),
                                           __builtin_amdgcn_perm(v.y, v.x, 0x07060302u), __builtin_amdgcn_perm(v.w, v.z, 0x07060302u)});
 }
-// Lane (n, g) = (l % 16, l / 16) holds dwords 0 .. 3 of 16-byte piece g; after it
-// the dwords g of pieces 0 .. 3.
-__device__ __forceinline__ u32x4 transpose4(u32x4 v) {
-  const auto a = __builtin_amdgcn_permlane32_swap(v.x, v.z, false, false);
-  const auto b = __builtin_amdgcn_permlane32_swap(v.y, v.w, false, false);
-  const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-  const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-  return u32x4{c[0], c[1], d[0], d[1]};
-}
-
-__device__ __forceinline__ float scale_at(const float* s, int i) { return s[i]; }
-__device__ __forceinline__ float scale_at(const uint16_t* s, int i) { return bf16_to_f32(s[i]); }
+// The N scales of a unit, as loaded, and the i-th of them.
+template <typename S, int N>
+struct Scales;
+template <int N>
+struct Scales<float, N> {
+  float v[N];
+  __device__ __forceinline__ void load(const float* p) { __builtin_memcpy(v, p, sizeof(v)); }
+  __device__ __forceinline__ void set(int i, float x) { v[i] = x; }
+  __device__ __forceinline__ float at(int i) const { return v[i]; }
+};
+template <int N>
+struct Scales<uint16_t, N> {
+  uint32_t v[N / 2];
+  __device__ __forceinline__ void load(const uint16_t* p) { __builtin_memcpy(v, p, sizeof(v)); }
+  __device__ __forceinline__ void set(int i, uint16_t x) {
+    v[i / 2] = i % 2 ? (v[i / 2] & 0xffffu) | (uint32_t(x) << 16) : x;
+  }
+  __device__ __forceinline__ float at(int i) const {
+    return __uint_as_float(i % 2 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
+  }
+};
 
 // 1 / (1 + e^-a) a from expf and a division, for fp32 results.
 __device__ __forceinline__ float silu_f32(float a) { return a / (1.f + expf(-a)); }
 
-// G: elements per scale; S: their type; BIAS: affine; NB: 16-row blocks of a tile.
-// K % G == 0, so K is a multiple of 32; past K, x is zero and the last codes and
-// scales are read again.
-template <int G, typename S, bool BIAS, int NB>
-__global__ __launch_bounds__(kWaves * kWave) void stream_kernel(Product p) {
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+// 16 bytes per lane straight into LDS, lane l's at `to` + 16 l.
+__device__ __forceinline__ void load_lds(const void* from, u32x4* to) {
+  __builtin_amdgcn_global_load_lds(from, (lds_ptr)to, 16, 0, 0);
+}
+// G: elements per scale; S: their type; BIAS: affine; NB: 16-row blocks of a tile;
+// KT: 16-column tiles of a wave (SwiGLU: half of them of w_up); WAVES of a
+// workgroup, each with its part of K: no wave waits for another before the end.
+//
+// K advances in units of two steps.  Loads are made in whole lines by consecutive
+// lanes (an L1 lookup serves 64 bytes of neighbouring lanes; in the operands' order,
+// 16 rows apart, each lane cost one), and LDS puts them in the operands' order: x
+// takes direct loads into it, 16 lanes a row and step; codes go to registers, 8 lanes
+// a row, and from there to LDS when their unit's turn comes.  A turn waits for all
+// that is on its way, takes both operands of its unit from LDS, asks for the next
+// unit, and multiplies meanwhile.
+// The 16-byte pieces of a row are swizzled by it (on the side of the global
+// addresses), so that 16 lanes that read the same piece of 16 rows meet 64 banks.
+// K % G == 0, so K is a multiple of 32; in a last, partial unit x is taken as zero
+// past K and the last codes and scales are read again.
+template <int G, typename S, bool BIAS, int NB, int KT, int WAVES>
+__global__ __launch_bounds__(WAVES * kWave, NB == 1 && !(G == 32 && BIAS) ? 2 : 1) void stream_kernel(Product p) {
   constexpr int kTM = 16 * NB;
   constexpr int kPer = kStep / G;      // groups in a step
-  constexpr bool kSplit = G < kStep;   // the four lanes of a weight row are in different groups
-  constexpr int kPitch = 16 * kT + 4;
-  __shared__ float s_sum[kWaves][kTM][kPitch];
+  constexpr int kSteps = kUnit / kStep;
+  constexpr bool kSplit = G < kStep;   // the four 32-element pieces of a step are in different groups
+  constexpr int kSlot = NB * 4 * kWave;        // 16-byte pieces of a step of x
+  constexpr int kCodes = KT * 2 * kWave;       // 16-byte pieces of a unit's codes
+  constexpr int kPitch = 16 * KT;              // floats of a row of partial sums, kept in s_x at the end
+  static_assert(kTM * kPitch * 4 <= kSteps * kSlot * 16, "the sums fit in s_x");
+  __shared__ u32x4 s_x[WAVES][kSteps][kSlot];
+  __shared__ u32x4 s_codes[WAVES][kCodes];
   __shared__ int s_rows[kTM];
 
   // workgroup b runs on XCD b % 8; XCD x takes row tiles x, x + 8, ..., all
@@ -94,50 +125,121 @@ __global__ __launch_bounds__(kWaves * kWave) void stream_kernel(Product p) {
   const Tile tile = p.direct ? direct_tile(m_idx, p.index, p.n_rows, p.n_experts, s_rows)
                              : find_tile<kTM>(m_idx, p.index, p.n_experts, p.n_rows);
   if (!tile.valid) return;             // whole workgroup
-  if (!p.direct && tid < kTM && tile.row0 + tid < tile.row_end)   // live rows
-    s_rows[tid] = p.order ? p.order[tile.row0 + tid] : tile.row0 + tid;
-  __syncthreads();
   // rows of the tile (row_end is the expert's); past them its first is read, and never stored
   const int live = tile.row_end - tile.row0 < kTM ? tile.row_end - tile.row0 : kTM;
+  if (!p.direct && tid < live) s_rows[tid] = p.order ? p.order[tile.row0 + tid] : tile.row0 + tid;
+  __syncthreads();
 
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int n = lane & 15, g = lane >> 4;
-  const int cols = p.glu ? 8 * kT : 16 * kT;   // output columns of the workgroup
+  const int cols = p.glu ? 8 * KT : 16 * KT;   // output columns of the workgroup
   const int col0 = grp * cols;
   const int n_scales = p.K / G;
+  const int units = p.K / kUnit;               // whole ones
+  const int first = int(int64_t(units) * wave / WAVES), last = int(int64_t(units) * (wave + 1) / WAVES);
 
-  const uint16_t* x_ptr[NB];
+  // weight row of row i of tile t, counted from the expert's first
+  auto row_of = [&](int t, int i) {
+    const int c = col0 + 16 * (p.glu && t >= KT / 2 ? t - KT / 2 : t) + i;
+    return c < p.N ? c : p.N - 1;              // partial last group; never stored
+  };
+  auto of_up = [&](int t) { return p.glu && t >= KT / 2; };
+  const int64_t row0 = int64_t(tile.expert) * p.N;
+  const S *s_ptr[KT], *b_ptr[KT];
+  uint32_t w_off[KT][2];                       // from the workgroup's first row, below 2^28
+  const uint8_t* w_base[2] = {p.w[0] + (row0 + col0) * (p.K / 2), p.glu ? p.w[1] + (row0 + col0) * (p.K / 2) : nullptr};
 #pragma unroll
-  for (int i = 0; i < NB; ++i) x_ptr[i] = p.rows + int64_t(s_rows[16 * i + n < live ? 16 * i + n : 0]) * p.K;
-  const uint8_t* w_ptr[kT];
-  const S *s_ptr[kT], *b_ptr[kT];
+  for (int t = 0; t < KT; ++t) {
+    const int64_t row = row0 + row_of(t, n);
+    s_ptr[t] = static_cast<const S*>(of_up(t) ? p.s[1] : p.s[0]) + row * n_scales;
+    b_ptr[t] = BIAS ? static_cast<const S*>(of_up(t) ? p.b[1] : p.b[0]) + row * n_scales : nullptr;
 #pragma unroll
-  for (int t = 0; t < kT; ++t) {
-    const int up = p.glu && t >= kT / 2;
-    int c = col0 + 16 * (up ? t - kT / 2 : t) + n;
-    if (c >= p.N) c = p.N - 1;                 // partial last group; never stored
-    const int64_t row = int64_t(tile.expert) * p.N + c;
-    w_ptr[t] = (up ? p.w[1] : p.w[0]) + row * (p.K / 2);
-    s_ptr[t] = static_cast<const S*>(up ? p.s[1] : p.s[0]) + row * n_scales;
-    b_ptr[t] = BIAS ? static_cast<const S*>(up ? p.b[1] : p.b[0]) + row * n_scales : nullptr;
+    for (int h = 0; h < 2; ++h) {
+      const int i = 8 * h + lane / 8;          // its row of the tile, piece lane % 8 ^ i / 2
+      w_off[t][h] = uint32_t(row_of(t, i) - col0) * uint32_t(p.K / 2) + 16 * ((lane % 8) ^ (i / 2));
+    }
   }
-
-  f32x4 acc[NB][kT];
+  const uint16_t* x_ptr[NB][4];
 #pragma unroll
   for (int i = 0; i < NB; ++i)
 #pragma unroll
-    for (int t = 0; t < kT; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < 4; ++j) {
+      const int r = 4 * j + lane / 16;         // row of the block, piece lane % 16 ^ r
+      x_ptr[i][j] = p.rows + int64_t(s_rows[16 * i + r < live ? 16 * i + r : 0]) * p.K + 8 * ((lane % 16) ^ r);
+    }
 
-  // one step: codes q, scales and biases of its groups, x as four A operands
+  f32x4 acc[NB][KT];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int t = 0; t < KT; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  struct Unit {
+    u32x4 q[KT][2];                            // rows 8 h + l / 8 of tile t
+    Scales<S, kUnit / G> s[KT], b[KT];
+  };
+  auto load_x = [&](int unit) {
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          load_lds(x_ptr[i][j] + (int64_t(unit) * kUnit + kStep * st), &s_x[wave][st][(4 * i + j) * kWave]);
+  };
+  auto load_w = [&](int unit, Unit& u) {
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      u.s[t].load(s_ptr[t] + int64_t(unit) * (kUnit / G));
+      if (BIAS) u.b[t].load(b_ptr[t] + int64_t(unit) * (kUnit / G));
+    }
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        u.q[t][h] = *reinterpret_cast<const u32x4*>((of_up(t) ? w_base[1] : w_base[0]) + int64_t(unit) * (kUnit / 2) + w_off[t][h]);
+  };
+  struct Operands {
+    u32x4 x[kSteps][NB][4], q[kSteps][KT];
+  };
+  auto take = [&](const Unit& u, Operands& o) {
+    u32x4* codes = s_codes[wave];
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) codes[(2 * t + h) * kWave + lane] = u.q[t][h];
+    // MFMA j takes from lane (n, g) the 8 elements of piece 4 j + g of x, or 4 g + j,
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          o.x[st][i][j] = s_x[wave][st][4 * i * kWave + 16 * n + ((kSplit ? 4 * j + g : 4 * g + j) ^ n)];
+    // and the codes in dword g of piece 4 st + j, or dword j of piece 4 st + g
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+      for (int t = 0; t < KT; ++t) {
+        const u32x4* row = codes + 2 * t * kWave + 8 * n;
+        if constexpr (kSplit) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            o.q[st][t][j] = reinterpret_cast<const uint32_t*>(row + ((4 * st + j) ^ (n / 2)))[g];
+        } else {
+          o.q[st][t] = row[(4 * st + g) ^ (n / 2)];
+        }
+      }
+  };
+
   const uint32_t c1 = BIAS ? 0x3f803f80u : 0xc100c100u;        // 1, or -8, twice in bf16
   const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{c1, c1, c1, c1});
-  auto multiply = [&](const u32x4 (&q)[kT], const float (&sc)[kT][kPer], const float (&bi)[kT][kPer],
-                      const u32x4 (&x)[NB][4]) {
+  auto multiply = [&](const Operands& o, const Scales<S, kUnit / G> (&us)[KT], const Scales<S, kUnit / G> (&ub)[KT], int st) {
     bf16x8 a[NB][4];
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) a[i][j] = evens_odds(x[i][j]);
+      for (int j = 0; j < 4; ++j) a[i][j] = evens_odds(o.x[st][i][j]);
     f32x4 sum[NB][kPer];                       // X, or -8 X
 #pragma unroll
     for (int i = 0; i < NB; ++i)
@@ -149,11 +251,10 @@ __global__ __launch_bounds__(kWaves * kWave) void stream_kernel(Product p) {
           sum[i][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i][h * (4 / kPer) + j], ones, sum[i][h], 0, 0, 0);
       }
 #pragma unroll
-    for (int t = 0; t < kT; ++t) {
-      const u32x4 v = kSplit ? transpose4(q[t]) : q[t];
+    for (int t = 0; t < KT; ++t) {
       bf16x8 b[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = codes8(v[j]);
+      for (int j = 0; j < 4; ++j) b[j] = codes8(o.q[st][t][j]);
 #pragma unroll
       for (int i = 0; i < NB; ++i)
 #pragma unroll
@@ -162,70 +263,98 @@ __global__ __launch_bounds__(kWaves * kWave) void stream_kernel(Product p) {
 #pragma unroll
           for (int j = 0; j < 4 / kPer; ++j)
             d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i][h * (4 / kPer) + j], b[h * (4 / kPer) + j], d, 0, 0, 0);
+          const float sc = us[t].at(st * kPer + h);
 #pragma unroll
-          for (int v4 = 0; v4 < 4; ++v4) {
-            acc[i][t][v4] = fmaf(sc[t][h], d[v4], acc[i][t][v4]);
-            if (BIAS) acc[i][t][v4] = fmaf(bi[t][h], sum[i][h][v4], acc[i][t][v4]);
+          for (int r = 0; r < 4; ++r) {
+            acc[i][t][r] = fmaf(sc, d[r], acc[i][t][r]);
+            if (BIAS) acc[i][t][r] = fmaf(ub[t].at(st * kPer + h), sum[i][h][r], acc[i][t][r]);
           }
         }
     }
   };
 
-  const int pieces = p.K / 32;
-  auto load = [&](int step, u32x4 (&q)[kT], float (&sc)[kT][kPer], float (&bi)[kT][kPer], u32x4 (&x)[NB][4]) {
-    const int piece = 4 * step + g;
-    const int at = piece < pieces ? piece : pieces - 1;
+  if (first < last) {
+    Unit u;
+    Operands o;
+    load_w(first, u);
+    load_x(first);
+    for (int at = first; at < last; ++at) {
+      __builtin_amdgcn_s_waitcnt(0x0f70);      // every load has landed
+      take(u, o);
+      Scales<S, kUnit / G> us[KT], ub[KT];
 #pragma unroll
-    for (int t = 0; t < kT; ++t) {
-      q[t] = *reinterpret_cast<const u32x4*>(w_ptr[t] + 16 * at);
+      for (int t = 0; t < KT; ++t) { us[t] = u.s[t]; ub[t] = u.b[t]; }
+      __builtin_amdgcn_s_waitcnt(0xc07f);      // and is read from LDS before more is asked for
+      __builtin_amdgcn_sched_barrier(0);
+      if (at + 1 < last) {
+        load_w(at + 1, u);
+        load_x(at + 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int h = 0; h < kPer; ++h) {
-        const int k = step * kPer + h < n_scales ? step * kPer + h : n_scales - 1;
-        sc[t][h] = scale_at(s_ptr[t], k);
-        bi[t][h] = BIAS ? scale_at(b_ptr[t], k) : 0.f;
+      for (int st = 0; st < kSteps; ++st) multiply(o, us, ub, st);
+    }
+  }
+  if (p.K % kUnit != 0 && wave == WAVES - 1) {
+    // the operands in place: lane (n, g) loads its own
+    Scales<S, kUnit / G> us[KT], ub[KT];
+    Operands o;
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st) {
+      const int k0 = units * kUnit + st * kStep;
+#pragma unroll
+      for (int t = 0; t < KT; ++t) {
+        const uint8_t* row = (of_up(t) ? p.w[1] : p.w[0]) + (row0 + row_of(t, n)) * (p.K / 2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = k0 + (kSplit ? 32 * j + 8 * g : 32 * g + 8 * j);
+          o.q[st][t][j] = *reinterpret_cast<const uint32_t*>(row + (k < p.K ? k : 0) / 2);
+        }
+#pragma unroll
+        for (int h = 0; h < kPer; ++h) {
+          const int k = k0 / G + h < n_scales ? k0 / G + h : n_scales - 1;
+          us[t].set(st * kPer + h, s_ptr[t][k]);
+          if (BIAS) ub[t].set(st * kPer + h, b_ptr[t][k]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const uint16_t* row = p.rows + int64_t(s_rows[16 * i + n < live ? 16 * i + n : 0]) * p.K;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = k0 + (kSplit ? 32 * j + 8 * g : 32 * g + 8 * j);
+          o.x[st][i][j] = k < p.K ? *reinterpret_cast<const u32x4*>(row + k) : u32x4{0, 0, 0, 0};
+        }
       }
     }
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = kSplit ? kStep * step + 32 * j + 8 * g : kStep * step + 32 * g + 8 * j;
-        x[i][j] = k < p.K ? *reinterpret_cast<const u32x4*>(x_ptr[i] + k) : u32x4{0, 0, 0, 0};
-      }
-  };
-
-  const int n_steps = (p.K + kStep - 1) / kStep;
-  const int first = int(int64_t(n_steps) * wave / kWaves), last = int(int64_t(n_steps) * (wave + 1) / kWaves);
-  for (int step = first; step < last; ++step) {
-    u32x4 q[kT], x[NB][4];
-    float sc[kT][kPer], bi[kT][kPer];
-    load(step, q, sc, bi, x);
-    multiply(q, sc, bi, x);
+    for (int st = 0; st < kSteps; ++st) multiply(o, us, ub, st);
   }
 
-  // the four quarters of K, added in order: lane (n, g) holds rows 4 g .. 4 g + 3
-  // of column n of each 16 x 16 tile
+  // the parts of K, added in order: lane (n, g) holds rows 4 g .. 4 g + 3 of column
+  // n of each 16 x 16 tile; columns are swizzled by the row's g, which keeps the
+  // four of them in different banks
+  auto swizzled = [](int row, int col) { return row * kPitch + (col ^ (16 * (row / 4 % KT))); };
+  float* mine = reinterpret_cast<float*>(s_x[wave]);
 #pragma unroll
   for (int i = 0; i < NB; ++i)
 #pragma unroll
-    for (int t = 0; t < kT; ++t)
+    for (int t = 0; t < KT; ++t)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) s_sum[wave][16 * i + 4 * g + v][16 * t + n] = acc[i][t][v];
+      for (int v = 0; v < 4; ++v) mine[swizzled(16 * i + 4 * g + v, 16 * t + n)] = acc[i][t][v];
   __syncthreads();
   const int quads = cols / 4;
-  for (int at = tid; at < live * quads; at += kWaves * kWave) {
+  for (int at = tid; at < live * quads; at += WAVES * kWave) {
     const int r = at / quads, c = at % quads * 4;
+    f32x4 a = {0.f, 0.f, 0.f, 0.f}, u = a;
+    for (int k = 0; k < WAVES; ++k) {
+      const float* part = reinterpret_cast<const float*>(s_x[k]);
+      a += *reinterpret_cast<const f32x4*>(part + swizzled(r, c));
+      if (p.glu) u += *reinterpret_cast<const f32x4*>(part + swizzled(r, 8 * KT + c));
+    }
     float o[4];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      float a = 0.f, u = 0.f;
-#pragma unroll
-      for (int k = 0; k < kWaves; ++k) {
-        a += s_sum[k][r][c + v];
-        if (p.glu) u += s_sum[k][r][8 * kT + c + v];
-      }
-      o[v] = p.glu ? (p.y_bf16 ? silu(a) : silu_f32(a)) * u : a;
-    }
+    for (int v = 0; v < 4; ++v) o[v] = p.glu ? (p.y_bf16 ? silu(a[v]) : silu_f32(a[v])) * u[v] : a[v];
     const int64_t row = int64_t(s_rows[r]) * p.N;
     if (p.y_bf16) {
       store4(static_cast<uint16_t*>(p.y) + row, col0 + c, p.N, p.N % 4 == 0, o);
@@ -240,9 +369,11 @@ __global__ __launch_bounds__(kWaves * kWave) void stream_kernel(Product p) {
 
 // Mean rows per expert from which a tile holds 32 rows.
 constexpr int64_t kNarrowRows = 10;
+// Workgroups up to which K is split over 8 waves, and a wave has half the columns.
+constexpr int64_t kFewBlocks = 256;
 
 struct Shape {
-  bool direct;
+  bool direct, deep;                   // deep: 8 waves split K
   int nb, col_groups;
   int64_t blocks;
 };
@@ -250,29 +381,33 @@ Shape shape_of(const Int4Product& g) {
   Shape s{};
   s.nb = g.n_rows < kNarrowRows * g.n_experts ? 1 : 2;
   s.direct = s.nb == 1 && g.n_rows <= kDirectRows;
-  const int cols = g.w_up ? 8 * kT : 16 * kT;
-  s.col_groups = int((g.n_dim + cols - 1) / cols);
-  s.blocks = (most_tiles(g.n_rows, g.n_experts, 16 * s.nb) + kXcds - 1) / kXcds * kXcds * s.col_groups;
+  const auto size = [&](int kt) {
+    const int cols = g.w_up ? 8 * kt : 16 * kt;
+    s.col_groups = int((g.n_dim + cols - 1) / cols);
+    s.blocks = (most_tiles(g.n_rows, g.n_experts, 16 * s.nb) + kXcds - 1) / kXcds * kXcds * s.col_groups;
+  };
+  size(4);
+  s.deep = s.nb == 1 && most_tiles(g.n_rows, g.n_experts, 16) * s.col_groups <= kFewBlocks;
+  if (s.deep) size(2);
   return s;
 }
 
 template <int G>
 void launch_group(const Product& p, const Shape& s, bool scales_bf16, hipStream_t stream) {
-  const auto go = [&](auto* type, auto bias, auto nb) {
+  const auto form = [&](auto* type, auto bias) {
     using S = std::remove_pointer_t<decltype(type)>;
-    stream_kernel<G, S, decltype(bias)::value, decltype(nb)::value>
-        <<<unsigned(s.blocks), kWaves * kWave, 0, stream>>>(p);
+    constexpr bool B = decltype(bias)::value;
+    const unsigned blocks = unsigned(s.blocks);
+    if (s.deep) stream_kernel<G, S, B, 1, 2, 8><<<blocks, 8 * kWave, 0, stream>>>(p);
+    else if (s.nb == 1) stream_kernel<G, S, B, 1, 4, 4><<<blocks, 4 * kWave, 0, stream>>>(p);
+    else stream_kernel<G, S, B, 2, 4, 4><<<blocks, 4 * kWave, 0, stream>>>(p);
   };
-  const auto rows = [&](auto* type, auto bias) {
-    if (s.nb == 1) go(type, bias, std::integral_constant<int, 1>());
-    else go(type, bias, std::integral_constant<int, 2>());
+  const auto type = [&](auto* t) {
+    if (p.b[0]) form(t, std::true_type());
+    else form(t, std::false_type());
   };
-  const auto form = [&](auto* type) {
-    if (p.b[0]) rows(type, std::true_type());
-    else rows(type, std::false_type());
-  };
-  if (scales_bf16) form(static_cast<uint16_t*>(nullptr));
-  else form(static_cast<float*>(nullptr));
+  if (scales_bf16) type(static_cast<uint16_t*>(nullptr));
+  else type(static_cast<float*>(nullptr));
 }
 
 }  // namespace
