@@ -29,6 +29,12 @@ typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kStep = 128;             // elements of K that one 16-byte load per lane covers
 constexpr int kUnit = 256;             // elements of K asked for together: whole lines of a weight row
 
+// Bytes of scales and biases of a weight row in a unit.  They share the registers
+// with the codes: from some number on (where the compiler would spill) a SIMD holds
+// one wave of a kernel.
+template <int G, typename S, bool BIAS>
+constexpr int kScaleBytes = (BIAS ? 2 : 1) * int(sizeof(S)) * kUnit / G;
+
 struct Product {
   const uint16_t* rows;
   int n_rows, K;
@@ -57,30 +63,56 @@ __device__ __forceinline__ bf16x8 evens_odds(u32x4 v) {
   return __builtin_bit_cast(bf16x8, u32x4{__builtin_amdgcn_perm(v.y, v.x, 0x05040100u), __builtin_amdgcn_perm(v.w, v.z, 0x05040100u),
                                           __builtin_amdgcn_perm(v.y, v.x, 0x07060302u), __builtin_amdgcn_perm(v.w, v.z, 0x07060302u)});
 }
-// The N scales of a unit, as loaded, and the i-th of them.
+// The N scales of a unit, as loaded, and the i-th of them.  They may begin at any
+// element.
 template <typename S, int N>
-struct Scales;
-template <int N>
-struct Scales<float, N> {
-  float v[N];
-  __device__ __forceinline__ void load(const float* p) { __builtin_memcpy(v, p, sizeof(v)); }
-  __device__ __forceinline__ void set(int i, float x) { v[i] = x; }
-  __device__ __forceinline__ float at(int i) const { return v[i]; }
-};
-template <int N>
-struct Scales<uint16_t, N> {
-  uint32_t v[N / 2];
-  __device__ __forceinline__ void load(const uint16_t* p) { __builtin_memcpy(v, p, sizeof(v)); }
-  __device__ __forceinline__ void set(int i, uint16_t x) {
-    v[i / 2] = i % 2 ? (v[i / 2] & 0xffffu) | (uint32_t(x) << 16) : x;
+struct Scales {
+  static constexpr int kWords = N * int(sizeof(S)) / 4;
+  typedef uint32_t Words __attribute__((ext_vector_type(kWords)));
+  typedef Words AnyWords __attribute__((aligned(sizeof(S))));
+  Words v;
+  __device__ __forceinline__ void load(const S* p) { v = *reinterpret_cast<const AnyWords*>(p); }
+  __device__ __forceinline__ void set(int i, S x) {
+    if constexpr (sizeof(S) == 4) v[i] = __builtin_bit_cast(uint32_t, x);
+    else v[i / 2] = i % 2 ? (v[i / 2] & 0xffffu) | (uint32_t(x) << 16) : uint32_t(x);
   }
   __device__ __forceinline__ float at(int i) const {
-    return __uint_as_float(i % 2 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
+    if constexpr (sizeof(S) == 4) return __uint_as_float(v[i]);
+    else return __uint_as_float(i % 2 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
   }
 };
 
 // 1 / (1 + e^-a) a from expf and a division, for fp32 results.
 __device__ __forceinline__ float silu_f32(float a) { return a / (1.f + expf(-a)); }
+
+// One step of 16 rows: a their A operands, b the codes of the KT tiles as B operands,
+// us and ub the scales and biases of the unit's groups, ST the step of it.
+template <int G, typename S, bool BIAS, int KT, int ST>
+__device__ __forceinline__ void multiply(f32x4 (&acc)[KT], const bf16x8 (&a)[4], const bf16x8 (&b)[KT][4],
+                                         const Scales<S, kUnit / G> (&us)[KT], const Scales<S, kUnit / G> (&ub)[KT]) {
+  constexpr int kPer = kStep / G, kChain = 4 / kPer;           // groups of a step, MFMAs of a group
+  constexpr uint32_t c = BIAS ? 0x3f803f80u : 0xc100c100u;     // 1, or -8, twice in bf16
+  const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{c, c, c, c});
+#pragma unroll
+  for (int h = 0; h < kPer; ++h) {
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};          // X, or -8 X
+#pragma unroll
+    for (int j = 0; j < kChain; ++j)
+      sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[h * kChain + j], ones, sum, 0, 0, 0);
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      f32x4 d = BIAS ? f32x4{0.f, 0.f, 0.f, 0.f} : sum;
+#pragma unroll
+      for (int j = 0; j < kChain; ++j)
+        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[h * kChain + j], b[t][h * kChain + j], d, 0, 0, 0);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        acc[t][r] = fmaf(us[t].at(ST * kPer + h), d[r], acc[t][r]);
+        if (BIAS) acc[t][r] = fmaf(ub[t].at(ST * kPer + h), sum[r], acc[t][r]);
+      }
+    }
+  }
+}
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
@@ -104,7 +136,7 @@ __device__ __forceinline__ void load_lds(const void* from, u32x4* to) {
 // K % G == 0, so K is a multiple of 32; in a last, partial unit x is taken as zero
 // past K and the last codes and scales are read again.
 template <int G, typename S, bool BIAS, int NB, int KT, int WAVES>
-__global__ __launch_bounds__(WAVES * kWave, NB == 1 && !(G == 32 && BIAS) ? 2 : 1) void stream_kernel(Product p) {
+__global__ __launch_bounds__(WAVES * kWave, (NB == 1 && (kScaleBytes<G, S, BIAS> <= 16 || KT == 2) ? 2 : 1)) void stream_kernel(Product p) {
   constexpr int kTM = 16 * NB;
   constexpr int kPer = kStep / G;      // groups in a step
   constexpr int kSteps = kUnit / kStep;
@@ -232,47 +264,25 @@ __global__ __launch_bounds__(WAVES * kWave, NB == 1 && !(G == 32 && BIAS) ? 2 : 
       }
   };
 
-  const uint32_t c1 = BIAS ? 0x3f803f80u : 0xc100c100u;        // 1, or -8, twice in bf16
-  const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{c1, c1, c1, c1});
-  auto multiply = [&](const Operands& o, const Scales<S, kUnit / G> (&us)[KT], const Scales<S, kUnit / G> (&ub)[KT], int st) {
-    bf16x8 a[NB][4];
+  auto step = [&](const Operands& o, const Scales<S, kUnit / G> (&us)[KT], const Scales<S, kUnit / G> (&ub)[KT], auto which) __attribute__((always_inline)) {
+    constexpr int st = decltype(which)::value;
+    bf16x8 b[KT][4];
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
+    for (int t = 0; t < KT; ++t)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) a[i][j] = evens_odds(o.x[st][i][j]);
-    f32x4 sum[NB][kPer];                       // X, or -8 X
+      for (int j = 0; j < 4; ++j) b[t][j] = codes8(o.q[st][t][j]);
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
+    for (int i = 0; i < NB; ++i) {
+      bf16x8 a[4];
 #pragma unroll
-      for (int h = 0; h < kPer; ++h) {
-        sum[i][h] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < 4 / kPer; ++j)
-          sum[i][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i][h * (4 / kPer) + j], ones, sum[i][h], 0, 0, 0);
-      }
-#pragma unroll
-    for (int t = 0; t < KT; ++t) {
-      bf16x8 b[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = codes8(o.q[st][t][j]);
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-#pragma unroll
-        for (int h = 0; h < kPer; ++h) {
-          f32x4 d = BIAS ? f32x4{0.f, 0.f, 0.f, 0.f} : sum[i][h];
-#pragma unroll
-          for (int j = 0; j < 4 / kPer; ++j)
-            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i][h * (4 / kPer) + j], b[h * (4 / kPer) + j], d, 0, 0, 0);
-          const float sc = us[t].at(st * kPer + h);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            acc[i][t][r] = fmaf(sc, d[r], acc[i][t][r]);
-            if (BIAS) acc[i][t][r] = fmaf(ub[t].at(st * kPer + h), sum[i][h][r], acc[i][t][r]);
-          }
-        }
+      for (int j = 0; j < 4; ++j) a[j] = evens_odds(o.x[st][i][j]);
+      multiply<G, S, BIAS, KT, st>(acc[i], a, b, us, ub);
     }
   };
-
+  auto both_steps = [&](const Operands& o, const Scales<S, kUnit / G> (&us)[KT], const Scales<S, kUnit / G> (&ub)[KT]) __attribute__((always_inline)) {
+    step(o, us, ub, std::integral_constant<int, 0>());
+    step(o, us, ub, std::integral_constant<int, 1>());
+  };
   if (first < last) {
     Unit u;
     Operands o;
@@ -291,8 +301,7 @@ __global__ __launch_bounds__(WAVES * kWave, NB == 1 && !(G == 32 && BIAS) ? 2 : 
         load_x(at + 1);
       }
       __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int st = 0; st < kSteps; ++st) multiply(o, us, ub, st);
+      both_steps(o, us, ub);
     }
   }
   if (p.K % kUnit != 0 && wave == WAVES - 1) {
@@ -327,8 +336,7 @@ __global__ __launch_bounds__(WAVES * kWave, NB == 1 && !(G == 32 && BIAS) ? 2 : 
         }
       }
     }
-#pragma unroll
-    for (int st = 0; st < kSteps; ++st) multiply(o, us, ub, st);
+    both_steps(o, us, ub);
   }
 
   // the parts of K, added in order: lane (n, g) holds rows 4 g .. 4 g + 3 of column
@@ -367,13 +375,268 @@ __global__ __launch_bounds__(WAVES * kWave, NB == 1 && !(G == 32 && BIAS) ? 2 : 
   }
 }
 
+// Many tiles: the waves of a workgroup take 16 KT columns each over the whole K and
+// share x, double-buffered in LDS, one barrier a unit.  Codes go to registers two
+// units ahead and through the wave's own LDS into the operands' order, as above; x
+// one unit ahead, its elements brought into the codes' order on the way.
+// Scales are asked for 32 bytes of a row at a time, for up to 8 units: unit by unit
+// the same lines came from L2 again each time, as much as the codes themselves (1024
+// rows, 256 experts, K 7168, F 2048: 807 us, 713 without these loads).
+template <int G, typename S, bool BIAS, int NB, int KT>
+__global__ __launch_bounds__(256, (NB * kScaleBytes<G, S, BIAS> <= 64 ? 2 : 1)) void wide_kernel(Product p) {
+  constexpr int kWaves = 4, kThreads = kWaves * kWave;
+  constexpr int kTM = 16 * NB;
+  constexpr bool kSplit = G < kStep;
+  constexpr int kPieces = kUnit / 8;           // 16-byte pieces of a row of x in a unit
+  constexpr int kLoads = kTM * kPieces / kThreads;
+  __shared__ u32x4 s_x[2][kTM * kPieces];
+  __shared__ u32x4 s_codes[kWaves][KT * 2 * kWave];
+  constexpr int kRowBytes = 32;                // of a row's scales in a chunk, two lanes a row
+  constexpr int kPerChunk = kRowBytes / int(sizeof(S)), kPerUnit = kUnit / G;
+  constexpr int kChunkUnits = kPerChunk / kPerUnit;
+  static_assert(KT * 16 * kRowBytes == kWave * 16, "16 bytes per lane");
+  __shared__ u32x4 s_scales[kWaves][BIAS ? 2 : 1][kWave];
+  __shared__ int s_rows[kTM];
+
+  const int slot = blockIdx.x / kXcds;
+  const int m_idx = (slot / p.n_groups) * kXcds + blockIdx.x % kXcds, grp = slot % p.n_groups;
+  const int tid = threadIdx.x, lane = lane_id();
+  const Tile tile = p.direct ? direct_tile(m_idx, p.index, p.n_rows, p.n_experts, s_rows)
+                             : find_tile<kTM>(m_idx, p.index, p.n_experts, p.n_rows);
+  if (!tile.valid) return;             // whole workgroup
+  // rows of the tile (row_end is the expert's); past them its first is read, and never stored
+  const int live = tile.row_end - tile.row0 < kTM ? tile.row_end - tile.row0 : kTM;
+  if (!p.direct && tid < live) s_rows[tid] = p.order ? p.order[tile.row0 + tid] : tile.row0 + tid;
+  __syncthreads();
+
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int n = lane & 15, g = lane >> 4;
+  const int cols = p.glu ? 8 * KT : 16 * KT;   // output columns of the wave
+  const int col0 = (grp * kWaves + wave) * cols;
+  const int n_scales = p.K / G;
+  const int units = p.K / kUnit;               // whole ones
+
+  // weight row of row i of tile t, counted from the expert's first
+  auto row_of = [&](int t, int i) {
+    const int c = col0 + 16 * (p.glu && t >= KT / 2 ? t - KT / 2 : t) + i;
+    return c < p.N ? c : p.N - 1;              // partial last group; never stored
+  };
+  auto of_up = [&](int t) { return p.glu && t >= KT / 2; };
+  const int64_t row0 = int64_t(tile.expert) * p.N;
+  const int base = row_of(0, 0);
+  // its row of the KT tiles' scales, 16-byte piece lane % 2 of a chunk
+  const int64_t s_row = (row0 + row_of(lane / 32, lane / 2 % 16)) * n_scales;
+  const S* s_ptr = static_cast<const S*>(of_up(lane / 32) ? p.s[1] : p.s[0]) + s_row;
+  const S* b_ptr = BIAS ? static_cast<const S*>(of_up(lane / 32) ? p.b[1] : p.b[0]) + s_row : nullptr;
+  uint32_t w_off[KT][2];                       // from the wave's first row, below 2^28
+  const uint8_t* w_base[2] = {p.w[0] + (row0 + base) * (p.K / 2), p.glu ? p.w[1] + (row0 + base) * (p.K / 2) : nullptr};
+#pragma unroll
+  for (int t = 0; t < KT; ++t) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = 8 * h + lane / 8;          // its row of the tile, piece lane % 8 ^ i / 2
+      w_off[t][h] = uint32_t(row_of(t, i) - base) * uint32_t(p.K / 2) + 16 * ((lane % 8) ^ (i / 2));
+    }
+  }
+  // row tid / 32 + 8 j of the tile, piece tid % 32
+  const uint16_t* x_ptr[kLoads];
+#pragma unroll
+  for (int j = 0; j < kLoads; ++j) {
+    const int r = tid / kPieces + 8 * j;
+    x_ptr[j] = p.rows + int64_t(s_rows[r < live ? r : 0]) * p.K + 8 * (tid % kPieces);
+  }
+
+  f32x4 acc[NB][KT];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int t = 0; t < KT; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  using Codes = u32x4[KT][2];                  // rows 8 h + l / 8 of tile t
+  using UnitScales = Scales<S, kPerUnit>;
+  auto load_x = [&](int unit, u32x4 (&x)[kLoads]) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) x[j] = *reinterpret_cast<const u32x4*>(x_ptr[j] + int64_t(unit) * kUnit);
+  };
+  auto put_x = [&](int buf, const u32x4 (&x)[kLoads]) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int r = tid / kPieces + 8 * j, piece = tid % kPieces;
+      s_x[buf][r * kPieces + (piece & 16) + ((piece ^ r) & 15)] = __builtin_bit_cast(u32x4, evens_odds(x[j]));
+    }
+  };
+  auto load_w = [&](int unit, Codes& q) {
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        q[t][h] = *reinterpret_cast<const u32x4*>((of_up(t) ? w_base[1] : w_base[0]) + int64_t(unit) * (kUnit / 2) + w_off[t][h]);
+  };
+  // this lane's 16 bytes of a chunk.  Past the row's end its last scale again if K
+  // ends inside a unit, which multiplies them by zero; else what comes behind, which
+  // no unit takes, as far as the tensor goes.
+  const int64_t behind = (int64_t(p.n_experts) * p.N - row0) * n_scales - (s_row - row0 * n_scales);
+  const int n_whole = p.K % kUnit != 0 ? n_scales : int(behind < (1 << 30) ? behind : 1 << 30);
+  auto load_piece = [&](const S* row, int chunk) {
+    constexpr int kIn = 16 / int(sizeof(S));
+    const int first = chunk * kPerChunk + kIn * (lane % 2);
+    S v[kIn];
+    if (first + kIn <= n_whole) {
+      __builtin_memcpy(v, row + first, 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kIn; ++i) v[i] = row[first + i < n_scales ? first + i : n_scales - 1];
+    }
+    return __builtin_bit_cast(u32x4, v);
+  };
+  auto load_scales = [&](int chunk, u32x4 (&c)[2]) {
+    c[0] = load_piece(s_ptr, chunk);
+    if (BIAS) c[1] = load_piece(b_ptr, chunk);
+  };
+  auto put_scales = [&](const u32x4 (&c)[2]) {
+#pragma unroll
+    for (int i = 0; i < (BIAS ? 2 : 1); ++i) s_scales[wave][i][lane] = c[i];
+  };
+  auto take_scales = [&](int unit, UnitScales (&us)[KT], UnitScales (&ub)[KT]) {
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      const int at = (16 * t + n) * kPerChunk + unit % kChunkUnits * kPerUnit;
+      us[t].load(reinterpret_cast<const S*>(s_scales[wave][0]) + at);
+      if (BIAS) ub[t].load(reinterpret_cast<const S*>(s_scales[wave][BIAS ? 1 : 0]) + at);
+    }
+  };
+  u32x4* codes = s_codes[wave];
+  auto put_w = [&](const Codes& q) {
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) codes[(2 * t + h) * kWave + lane] = q[t][h];
+  };
+  auto step = [&](int buf, const UnitScales (&us)[KT], const UnitScales (&ub)[KT], auto which) __attribute__((always_inline)) {
+    constexpr int st = decltype(which)::value;
+    // MFMA j takes from lane (n, g) the codes in dword g of piece 4 st + j, or dword j
+    // of piece 4 st + g, and the 8 elements of piece 4 j + g of x, or 4 g + j
+    bf16x8 b[KT][4];
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      const u32x4* row = codes + 2 * t * kWave + 8 * n;
+      u32x4 v;
+      if constexpr (kSplit) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = reinterpret_cast<const uint32_t*>(row + ((4 * st + j) ^ (n / 2)))[g];
+      } else {
+        v = row[(4 * st + g) ^ (n / 2)];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[t][j] = codes8(v[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      bf16x8 a[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        a[j] = __builtin_bit_cast(bf16x8, s_x[buf][(16 * i + n) * kPieces + 16 * st + ((kSplit ? 4 * j + g : 4 * g + j) ^ n)]);
+      multiply<G, S, BIAS, KT, st>(acc[i], a, b, us, ub);
+    }
+  };
+  auto both_steps = [&](int buf, const UnitScales (&us)[KT], const UnitScales (&ub)[KT]) __attribute__((always_inline)) {
+    step(buf, us, ub, std::integral_constant<int, 0>());
+    step(buf, us, ub, std::integral_constant<int, 1>());
+  };
+
+  const int all_units = (p.K + kUnit - 1) / kUnit;
+  u32x4 x[kLoads], chunk[2];
+  UnitScales us[KT], ub[KT];
+  load_scales(0, chunk);
+  __builtin_amdgcn_sched_barrier(0);
+  if (units > 0) {
+    Codes q0, q1;
+    load_x(0, x);
+    load_w(0, q0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_w(units > 1 ? 1 : 0, q1);
+    __builtin_amdgcn_sched_barrier(0);
+    put_x(0, x);
+    __syncthreads();
+    // units past the last one are the last one again, and are not used
+    auto turn = [&](int at, int buf, Codes& q) __attribute__((always_inline)) {
+      load_x(at + 1 < units ? at + 1 : units - 1, x);
+      __builtin_amdgcn_sched_barrier(0);
+      if (at % kChunkUnits == 0) {
+        put_scales(chunk);
+        if (at + kChunkUnits < all_units) load_scales(at / kChunkUnits + 1, chunk);
+      }
+      put_w(q);
+      take_scales(at, us, ub);
+      __builtin_amdgcn_sched_barrier(0);
+      load_w(at + 2 < units ? at + 2 : units - 1, q);
+      __builtin_amdgcn_sched_barrier(0);
+      both_steps(buf, us, ub);
+      __builtin_amdgcn_sched_barrier(0);
+      put_x(buf ^ 1, x);               // last read a unit ago, which every wave has left
+      __syncthreads();
+    };
+    int at = 0;
+    for (; at + 1 < units; at += 2) {
+      turn(at, 0, q0);
+      turn(at + 1, 1, q1);
+    }
+    if (at < units) turn(at, 0, q0);
+  }
+  if (p.K % kUnit != 0) {              // x is zero past K, and the last codes and scales are read again
+    Codes q;
+    const int k0 = units * kUnit;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+      x[j] = k0 + 8 * (tid % kPieces) < p.K ? *reinterpret_cast<const u32x4*>(x_ptr[j] + k0) : u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int piece = (lane % 8) ^ (4 * h + lane / 16);
+        const uint32_t off = k0 / 2 + 16 * piece < p.K / 2 ? uint32_t(k0 / 2) + w_off[t][h] : w_off[t][h] - 16 * piece;
+        q[t][h] = *reinterpret_cast<const u32x4*>((of_up(t) ? w_base[1] : w_base[0]) + off);
+      }
+    const int buf = units & 1;
+    if (units % kChunkUnits == 0) put_scales(chunk);
+    put_x(buf, x);
+    put_w(q);
+    take_scales(units, us, ub);
+    __syncthreads();
+    both_steps(buf, us, ub);
+  }
+
+  // lane (n, g) holds rows 4 g .. 4 g + 3 of column n of each 16 x 16 tile
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int at = 16 * i + 4 * g + r;
+      if (at >= live) continue;
+      const int64_t row = int64_t(s_rows[at]) * p.N;
+#pragma unroll
+      for (int t = 0; t < KT; ++t) {
+        const int c = col0 + 16 * t + n;
+        if (c >= p.N || (p.glu && t >= KT / 2)) continue;
+        const float a = acc[i][t][r], up = acc[i][(t + KT / 2) % KT][r];
+        const float o = p.glu ? (p.y_bf16 ? silu(a) : silu_f32(a)) * up : a;
+        if (p.y_bf16) static_cast<uint16_t*>(p.y)[row + c] = uint16_t(pack2(o, 0.f));
+        else static_cast<float*>(p.y)[row + c] = o;
+      }
+    }
+}
+
 // Mean rows per expert from which a tile holds 32 rows.
 constexpr int64_t kNarrowRows = 10;
-// Workgroups up to which K is split over 8 waves, and a wave has half the columns.
-constexpr int64_t kFewBlocks = 256;
+// Workgroups up to which K is split over 8 waves, and a wave has half the columns;
+// from which the waves split the columns.
+constexpr int64_t kFewBlocks = 256, kManyBlocks = 300;
+constexpr int kWideT = 2;
 
+enum class Form { kDeep, kSplitK, kWide };
 struct Shape {
-  bool direct, deep;                   // deep: 8 waves split K
+  bool direct;
+  Form form;
   int nb, col_groups;
   int64_t blocks;
 };
@@ -381,14 +644,12 @@ Shape shape_of(const Int4Product& g) {
   Shape s{};
   s.nb = g.n_rows < kNarrowRows * g.n_experts ? 1 : 2;
   s.direct = s.nb == 1 && g.n_rows <= kDirectRows;
-  const auto size = [&](int kt) {
-    const int cols = g.w_up ? 8 * kt : 16 * kt;
-    s.col_groups = int((g.n_dim + cols - 1) / cols);
-    s.blocks = (most_tiles(g.n_rows, g.n_experts, 16 * s.nb) + kXcds - 1) / kXcds * kXcds * s.col_groups;
-  };
-  size(4);
-  s.deep = s.nb == 1 && most_tiles(g.n_rows, g.n_experts, 16) * s.col_groups <= kFewBlocks;
-  if (s.deep) size(2);
+  const int64_t tiles = most_tiles(g.n_rows, g.n_experts, 16 * s.nb);
+  const auto groups = [&](int kt, int waves) { return (g.n_dim + (g.w_up ? 8 : 16) * kt * waves - 1) / ((g.w_up ? 8 : 16) * kt * waves); };
+  s.form = tiles * groups(kWideT, 4) >= kManyBlocks ? Form::kWide
+           : s.nb == 1 && tiles * groups(4, 1) <= kFewBlocks ? Form::kDeep : Form::kSplitK;
+  s.col_groups = int(s.form == Form::kWide ? groups(kWideT, 4) : groups(s.form == Form::kDeep ? 2 : 4, 1));
+  s.blocks = (tiles + kXcds - 1) / kXcds * kXcds * s.col_groups;
   return s;
 }
 
@@ -398,9 +659,11 @@ void launch_group(const Product& p, const Shape& s, bool scales_bf16, hipStream_
     using S = std::remove_pointer_t<decltype(type)>;
     constexpr bool B = decltype(bias)::value;
     const unsigned blocks = unsigned(s.blocks);
-    if (s.deep) stream_kernel<G, S, B, 1, 2, 8><<<blocks, 8 * kWave, 0, stream>>>(p);
-    else if (s.nb == 1) stream_kernel<G, S, B, 1, 4, 4><<<blocks, 4 * kWave, 0, stream>>>(p);
-    else stream_kernel<G, S, B, 2, 4, 4><<<blocks, 4 * kWave, 0, stream>>>(p);
+    if (s.form == Form::kDeep) stream_kernel<G, S, B, 1, 2, 8><<<blocks, 8 * kWave, 0, stream>>>(p);
+    else if (s.form == Form::kSplitK && s.nb == 1) stream_kernel<G, S, B, 1, 4, 4><<<blocks, 4 * kWave, 0, stream>>>(p);
+    else if (s.form == Form::kSplitK) stream_kernel<G, S, B, 2, 4, 4><<<blocks, 4 * kWave, 0, stream>>>(p);
+    else if (s.nb == 1) wide_kernel<G, S, B, 1, kWideT><<<blocks, 4 * kWave, 0, stream>>>(p);
+    else wide_kernel<G, S, B, 2, kWideT><<<blocks, 4 * kWave, 0, stream>>>(p);
   };
   const auto type = [&](auto* t) {
     if (p.b[0]) form(t, std::true_type());
