@@ -149,10 +149,7 @@ __global__ __launch_bounds__(WAVES * kWave, (NB == 1 && (kScaleBytes<G, S, BIAS>
   __shared__ u32x4 s_codes[WAVES][kCodes];
   __shared__ int s_rows[kTM];
 
-  // workgroup b runs on XCD b % 8; XCD x takes row tiles x, x + 8, ..., all
-  // column groups of one back to back
-  const int slot = blockIdx.x / kXcds;
-  const int m_idx = (slot / p.n_groups) * kXcds + blockIdx.x % kXcds, grp = slot % p.n_groups;
+  const int m_idx = blockIdx.x / p.n_groups, grp = blockIdx.x % p.n_groups;
   const int tid = threadIdx.x, lane = lane_id();
   const Tile tile = p.direct ? direct_tile(m_idx, p.index, p.n_rows, p.n_experts, s_rows)
                              : find_tile<kTM>(m_idx, p.index, p.n_experts, p.n_rows);
@@ -398,8 +395,7 @@ __global__ __launch_bounds__(256, (NB * kScaleBytes<G, S, BIAS> <= 64 ? 2 : 1)) 
   __shared__ u32x4 s_scales[kWaves][BIAS ? 2 : 1][kWave];
   __shared__ int s_rows[kTM];
 
-  const int slot = blockIdx.x / kXcds;
-  const int m_idx = (slot / p.n_groups) * kXcds + blockIdx.x % kXcds, grp = slot % p.n_groups;
+  const int m_idx = blockIdx.x / p.n_groups, grp = blockIdx.x % p.n_groups;
   const int tid = threadIdx.x, lane = lane_id();
   const Tile tile = p.direct ? direct_tile(m_idx, p.index, p.n_rows, p.n_experts, s_rows)
                              : find_tile<kTM>(m_idx, p.index, p.n_experts, p.n_rows);
@@ -649,7 +645,7 @@ Shape shape_of(const Int4Product& g) {
   s.form = tiles * groups(kWideT, 4) >= kManyBlocks ? Form::kWide
            : s.nb == 1 && tiles * groups(4, 1) <= kFewBlocks ? Form::kDeep : Form::kSplitK;
   s.col_groups = int(s.form == Form::kWide ? groups(kWideT, 4) : groups(s.form == Form::kDeep ? 2 : 4, 1));
-  s.blocks = (tiles + kXcds - 1) / kXcds * kXcds * s.col_groups;
+  s.blocks = tiles * s.col_groups;
   return s;
 }
 
