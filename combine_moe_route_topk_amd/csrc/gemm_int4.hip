@@ -82,33 +82,56 @@ struct Scales {
   }
 };
 
+template <int CTRL>
+__device__ __forceinline__ float row_step(float v) {
+  const int b = __float_as_int(v);
+  return __int_as_float(__builtin_amdgcn_update_dpp(b, b, CTRL, 0xF, 0xF, false));
+}
+// Sum of 8 elements of x.
+__device__ __forceinline__ float piece_sum(u32x4 x) {
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, x[i]), __builtin_bit_cast(bf16x2, 0x3f803f80u), sum, false);
+  return sum;
+}
+
 // 1 / (1 + e^-a) a from expf and a division, for fp32 results.
 __device__ __forceinline__ float silu_f32(float a) { return a / (1.f + expf(-a)); }
 
+// How the term (b or -8 s) X is added.
+//   kSym: a constant operand of -8 makes it the start of a group's sum.
+//   kFma: X by a constant operand of 1, then a multiply-add per group and result.
+//   kMfma (bf16 biases, wide_kernel): the matrix cores add it for 16 groups at a time
+//     from X as three bf16 terms, which hold all its 24 bits.
+enum class Bias { kSym, kFma, kMfma };
+
 // One step of 16 rows: a their A operands, b the codes of the KT tiles as B operands,
 // us and ub the scales and biases of the unit's groups, ST the step of it.
-template <int G, typename S, bool BIAS, int KT, int ST>
+template <int G, typename S, Bias HOW, int KT, int ST>
 __device__ __forceinline__ void multiply(f32x4 (&acc)[KT], const bf16x8 (&a)[4], const bf16x8 (&b)[KT][4],
                                          const Scales<S, kUnit / G> (&us)[KT], const Scales<S, kUnit / G> (&ub)[KT]) {
   constexpr int kPer = kStep / G, kChain = 4 / kPer;           // groups of a step, MFMAs of a group
-  constexpr uint32_t c = BIAS ? 0x3f803f80u : 0xc100c100u;     // 1, or -8, twice in bf16
+  constexpr uint32_t c = HOW == Bias::kSym ? 0xc100c100u : 0x3f803f80u;   // -8, or 1, twice in bf16
   const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{c, c, c, c});
 #pragma unroll
   for (int h = 0; h < kPer; ++h) {
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};          // X, or -8 X
+    if (HOW != Bias::kMfma) {
 #pragma unroll
-    for (int j = 0; j < kChain; ++j)
-      sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[h * kChain + j], ones, sum, 0, 0, 0);
+      for (int j = 0; j < kChain; ++j)
+        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[h * kChain + j], ones, sum, 0, 0, 0);
+    }
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
-      f32x4 d = BIAS ? f32x4{0.f, 0.f, 0.f, 0.f} : sum;
+      f32x4 d = HOW == Bias::kSym ? sum : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < kChain; ++j)
         d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[h * kChain + j], b[t][h * kChain + j], d, 0, 0, 0);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         acc[t][r] = fmaf(us[t].at(ST * kPer + h), d[r], acc[t][r]);
-        if (BIAS) acc[t][r] = fmaf(ub[t].at(ST * kPer + h), sum[r], acc[t][r]);
+        if (HOW == Bias::kFma) acc[t][r] = fmaf(ub[t].at(ST * kPer + h), sum[r], acc[t][r]);
       }
     }
   }
@@ -273,7 +296,7 @@ __global__ __launch_bounds__(WAVES * kWave, (NB == 1 && (kScaleBytes<G, S, BIAS>
       bf16x8 a[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) a[j] = evens_odds(o.x[st][i][j]);
-      multiply<G, S, BIAS, KT, st>(acc[i], a, b, us, ub);
+      multiply<G, S, BIAS ? Bias::kFma : Bias::kSym, KT, st>(acc[i], a, b, us, ub);
     }
   };
   auto both_steps = [&](const Operands& o, const Scales<S, kUnit / G> (&us)[KT], const Scales<S, kUnit / G> (&ub)[KT]) __attribute__((always_inline)) {
@@ -379,11 +402,15 @@ __global__ __launch_bounds__(WAVES * kWave, (NB == 1 && (kScaleBytes<G, S, BIAS>
 // Scales are asked for 32 bytes of a row at a time, for up to 8 units: unit by unit
 // the same lines came from L2 again each time, as much as the codes themselves (1024
 // rows, 256 experts, K 7168, F 2048: 807 us, 713 without these loads).
+// K is whole units and a row's scales whole 16 bytes (whole_rows below), so no load in
+// the loop has another form for the end of a row: the branch between two forms made
+// the compiler wait for every load there.
 template <int G, typename S, bool BIAS, int NB, int KT>
-__global__ __launch_bounds__(256, (NB * kScaleBytes<G, S, BIAS> <= 64 ? 2 : 1)) void wide_kernel(Product p) {
+__global__ __launch_bounds__(256, 2) void wide_kernel(Product p) {
   constexpr int kWaves = 4, kThreads = kWaves * kWave;
   constexpr int kTM = 16 * NB;
   constexpr bool kSplit = G < kStep;
+  constexpr Bias kHow = !BIAS ? Bias::kSym : sizeof(S) == 2 ? Bias::kMfma : Bias::kFma;
   constexpr int kPieces = kUnit / 8;           // 16-byte pieces of a row of x in a unit
   constexpr int kLoads = kTM * kPieces / kThreads;
   __shared__ u32x4 s_x[2][kTM * kPieces];
@@ -392,7 +419,11 @@ __global__ __launch_bounds__(256, (NB * kScaleBytes<G, S, BIAS> <= 64 ? 2 : 1)) 
   constexpr int kPerChunk = kRowBytes / int(sizeof(S)), kPerUnit = kUnit / G;
   constexpr int kChunkUnits = kPerChunk / kPerUnit;
   static_assert(KT * 16 * kRowBytes == kWave * 16, "16 bytes per lane");
-  __shared__ u32x4 s_scales[kWaves][BIAS ? 2 : 1][kWave];
+  __shared__ u32x4 s_scales[kWaves][kHow == Bias::kFma ? 2 : 1][kWave];
+  // kMfma: X of 16 groups, by row, in three bf16 terms; one block of groups is added
+  // while the next one's X are written
+  constexpr int kBlockUnits = 16 * G / kUnit;
+  __shared__ uint16_t s_sums[kHow == Bias::kMfma ? 2 : 1][3][kHow == Bias::kMfma ? kTM : 1][16];
   __shared__ int s_rows[kTM];
 
   const int m_idx = blockIdx.x / p.n_groups, grp = blockIdx.x % p.n_groups;
@@ -403,6 +434,10 @@ __global__ __launch_bounds__(256, (NB * kScaleBytes<G, S, BIAS> <= 64 ? 2 : 1)) 
   // rows of the tile (row_end is the expert's); past them its first is read, and never stored
   const int live = tile.row_end - tile.row0 < kTM ? tile.row_end - tile.row0 : kTM;
   if (!p.direct && tid < live) s_rows[tid] = p.order ? p.order[tile.row0 + tid] : tile.row0 + tid;
+  if constexpr (kHow == Bias::kMfma) {         // groups past K are multiplied by 0
+    uint16_t* sums = &s_sums[0][0][0][0];
+    for (int i = tid; i < 2 * 3 * kTM * 16; i += kThreads) sums[i] = 0;
+  }
   __syncthreads();
 
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -410,7 +445,7 @@ __global__ __launch_bounds__(256, (NB * kScaleBytes<G, S, BIAS> <= 64 ? 2 : 1)) 
   const int cols = p.glu ? 8 * KT : 16 * KT;   // output columns of the wave
   const int col0 = (grp * kWaves + wave) * cols;
   const int n_scales = p.K / G;
-  const int units = p.K / kUnit;               // whole ones
+  const int units = p.K / kUnit;
 
   // weight row of row i of tile t, counted from the expert's first
   auto row_of = [&](int t, int i) {
@@ -423,7 +458,7 @@ __global__ __launch_bounds__(256, (NB * kScaleBytes<G, S, BIAS> <= 64 ? 2 : 1)) 
   // its row of the KT tiles' scales, 16-byte piece lane % 2 of a chunk
   const int64_t s_row = (row0 + row_of(lane / 32, lane / 2 % 16)) * n_scales;
   const S* s_ptr = static_cast<const S*>(of_up(lane / 32) ? p.s[1] : p.s[0]) + s_row;
-  const S* b_ptr = BIAS ? static_cast<const S*>(of_up(lane / 32) ? p.b[1] : p.b[0]) + s_row : nullptr;
+  const S* b_ptr = kHow == Bias::kFma ? static_cast<const S*>(of_up(lane / 32) ? p.b[1] : p.b[0]) + s_row : nullptr;
   uint32_t w_off[KT][2];                       // from the wave's first row, below 2^28
   const uint8_t* w_base[2] = {p.w[0] + (row0 + base) * (p.K / 2), p.glu ? p.w[1] + (row0 + base) * (p.K / 2) : nullptr};
 #pragma unroll
@@ -454,11 +489,28 @@ __global__ __launch_bounds__(256, (NB * kScaleBytes<G, S, BIAS> <= 64 ? 2 : 1)) 
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) x[j] = *reinterpret_cast<const u32x4*>(x_ptr[j] + int64_t(unit) * kUnit);
   };
-  auto put_x = [&](int buf, const u32x4 (&x)[kLoads]) {
+  auto put_x = [&](int unit, const u32x4 (&x)[kLoads]) {
+    const int buf = unit & 1;
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
       const int r = tid / kPieces + 8 * j, piece = tid % kPieces;
       s_x[buf][r * kPieces + (piece & 16) + ((piece ^ r) & 15)] = __builtin_bit_cast(u32x4, evens_odds(x[j]));
+      if constexpr (kHow == Bias::kMfma) {     // the piece's sum, and its group's, G / 8 lanes side by side
+        float sum = piece_sum(x[j]);
+        sum += row_step<0xB1>(sum);            // lanes 1 0 3 2
+        sum += row_step<0x4E>(sum);            // lanes 2 3 0 1
+        if (G >= 64) sum += row_step<0x141>(sum);    // row_half_mirror
+        if (G >= 128) sum += row_step<0x140>(sum);   // row_mirror
+        if (piece % (G / 8) == 0) {
+          const int at = unit % kBlockUnits * (kUnit / G) + piece / (G / 8);
+#pragma unroll
+          for (int term = 0; term < 3; ++term) {
+            const uint32_t v = pack2(sum, 0.f);
+            s_sums[unit / kBlockUnits & 1][term][r][at] = uint16_t(v);
+            sum -= __uint_as_float(v << 16);
+          }
+        }
+      }
     }
   };
   auto load_w = [&](int unit, Codes& q) {
@@ -468,37 +520,53 @@ __global__ __launch_bounds__(256, (NB * kScaleBytes<G, S, BIAS> <= 64 ? 2 : 1)) 
       for (int h = 0; h < 2; ++h)
         q[t][h] = *reinterpret_cast<const u32x4*>((of_up(t) ? w_base[1] : w_base[0]) + int64_t(unit) * (kUnit / 2) + w_off[t][h]);
   };
-  // this lane's 16 bytes of a chunk.  Past the row's end its last scale again if K
-  // ends inside a unit, which multiplies them by zero; else what comes behind, which
-  // no unit takes, as far as the tensor goes.
-  const int64_t behind = (int64_t(p.n_experts) * p.N - row0) * n_scales - (s_row - row0 * n_scales);
-  const int n_whole = p.K % kUnit != 0 ? n_scales : int(behind < (1 << 30) ? behind : 1 << 30);
+  // this lane's 16 bytes of a chunk; of a last, partial chunk some lie behind the row
+  // and are not used: the row's first in their place
   auto load_piece = [&](const S* row, int chunk) {
-    constexpr int kIn = 16 / int(sizeof(S));
-    const int first = chunk * kPerChunk + kIn * (lane % 2);
-    S v[kIn];
-    if (first + kIn <= n_whole) {
-      __builtin_memcpy(v, row + first, 16);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kIn; ++i) v[i] = row[first + i < n_scales ? first + i : n_scales - 1];
-    }
-    return __builtin_bit_cast(u32x4, v);
+    const int first = chunk * kPerChunk + 16 / int(sizeof(S)) * (lane % 2);
+    return *reinterpret_cast<const u32x4*>(row + (first < n_scales ? first : 0));
   };
   auto load_scales = [&](int chunk, u32x4 (&c)[2]) {
     c[0] = load_piece(s_ptr, chunk);
-    if (BIAS) c[1] = load_piece(b_ptr, chunk);
+    if (kHow == Bias::kFma) c[1] = load_piece(b_ptr, chunk);
+  };
+  // kMfma: the biases of 16 groups, groups 4 g .. 4 g + 3 of row n of each tile, 0 past
+  // the row's end; and their products with these groups' X
+  uint2 biases[KT];
+  const uint16_t* bias_ptr[KT];
+#pragma unroll
+  for (int t = 0; t < KT; ++t)
+    bias_ptr[t] = kHow == Bias::kMfma ? static_cast<const uint16_t*>(of_up(t) ? p.b[1] : p.b[0]) + (row0 + row_of(t, n)) * n_scales : nullptr;
+  auto get_biases = [&](int unit) __attribute__((always_inline)) {
+    const int first = unit * kPerUnit + 4 * g;
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      const uint2 v = *reinterpret_cast<const uint2*>(bias_ptr[t] + (first < n_scales ? first : 0));
+      biases[t] = first < n_scales ? v : make_uint2(0u, 0u);
+    }
+  };
+  auto use_biases = [&](int unit) __attribute__((always_inline)) {
+    typedef short short4v __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int term = 0; term < 3; ++term) {
+        const short4v v = *reinterpret_cast<const short4v*>(&s_sums[unit / kBlockUnits & 1][term][16 * i + n][4 * g]);
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+          acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(v, __builtin_bit_cast(short4v, biases[t]), acc[i][t], 0, 0, 0);
+      }
   };
   auto put_scales = [&](const u32x4 (&c)[2]) {
 #pragma unroll
-    for (int i = 0; i < (BIAS ? 2 : 1); ++i) s_scales[wave][i][lane] = c[i];
+    for (int i = 0; i < (kHow == Bias::kFma ? 2 : 1); ++i) s_scales[wave][i][lane] = c[i];
   };
   auto take_scales = [&](int unit, UnitScales (&us)[KT], UnitScales (&ub)[KT]) {
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
       const int at = (16 * t + n) * kPerChunk + unit % kChunkUnits * kPerUnit;
       us[t].load(reinterpret_cast<const S*>(s_scales[wave][0]) + at);
-      if (BIAS) ub[t].load(reinterpret_cast<const S*>(s_scales[wave][BIAS ? 1 : 0]) + at);
+      if (kHow == Bias::kFma) ub[t].load(reinterpret_cast<const S*>(s_scales[wave][1]) + at);
     }
   };
   u32x4* codes = s_codes[wave];
@@ -528,80 +596,67 @@ __global__ __launch_bounds__(256, (NB * kScaleBytes<G, S, BIAS> <= 64 ? 2 : 1)) 
     }
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
+      if (i > 0 && 16 * i >= live) break;      // whole workgroup
       bf16x8 a[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         a[j] = __builtin_bit_cast(bf16x8, s_x[buf][(16 * i + n) * kPieces + 16 * st + ((kSplit ? 4 * j + g : 4 * g + j) ^ n)]);
-      multiply<G, S, BIAS, KT, st>(acc[i], a, b, us, ub);
+      multiply<G, S, kHow, KT, st>(acc[i], a, b, us, ub);
     }
+    // the products stay in their step: moved out of it they keep its operands alive
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int t = 0; t < KT; ++t) asm volatile("" : "+v"(acc[i][t])::"memory");
   };
   auto both_steps = [&](int buf, const UnitScales (&us)[KT], const UnitScales (&ub)[KT]) __attribute__((always_inline)) {
     step(buf, us, ub, std::integral_constant<int, 0>());
     step(buf, us, ub, std::integral_constant<int, 1>());
   };
 
-  const int all_units = (p.K + kUnit - 1) / kUnit;
   u32x4 x[kLoads], chunk[2];
   UnitScales us[KT], ub[KT];
   load_scales(0, chunk);
+  if (kHow == Bias::kMfma) get_biases(0);
   __builtin_amdgcn_sched_barrier(0);
-  if (units > 0) {
-    Codes q0, q1;
-    load_x(0, x);
-    load_w(0, q0);
+  Codes q0, q1;
+  load_x(0, x);
+  load_w(0, q0);
+  __builtin_amdgcn_sched_barrier(0);
+  load_w(units > 1 ? 1 : 0, q1);
+  __builtin_amdgcn_sched_barrier(0);
+  put_x(0, x);
+  __syncthreads();
+  // units past the last one are the last one again, and are not used
+  auto turn = [&](int at, int buf, Codes& q) __attribute__((always_inline)) {
+    load_x(at + 1 < units ? at + 1 : units - 1, x);
     __builtin_amdgcn_sched_barrier(0);
-    load_w(units > 1 ? 1 : 0, q1);
-    __builtin_amdgcn_sched_barrier(0);
-    put_x(0, x);
-    __syncthreads();
-    // units past the last one are the last one again, and are not used
-    auto turn = [&](int at, int buf, Codes& q) __attribute__((always_inline)) {
-      load_x(at + 1 < units ? at + 1 : units - 1, x);
-      __builtin_amdgcn_sched_barrier(0);
-      if (at % kChunkUnits == 0) {
-        put_scales(chunk);
-        if (at + kChunkUnits < all_units) load_scales(at / kChunkUnits + 1, chunk);
-      }
-      put_w(q);
-      take_scales(at, us, ub);
-      __builtin_amdgcn_sched_barrier(0);
-      load_w(at + 2 < units ? at + 2 : units - 1, q);
-      __builtin_amdgcn_sched_barrier(0);
-      both_steps(buf, us, ub);
-      __builtin_amdgcn_sched_barrier(0);
-      put_x(buf ^ 1, x);               // last read a unit ago, which every wave has left
-      __syncthreads();
-    };
-    int at = 0;
-    for (; at + 1 < units; at += 2) {
-      turn(at, 0, q0);
-      turn(at + 1, 1, q1);
+    if (at % kChunkUnits == 0) {
+      put_scales(chunk);
+      load_scales(at / kChunkUnits + 1, chunk);
     }
-    if (at < units) turn(at, 0, q0);
-  }
-  if (p.K % kUnit != 0) {              // x is zero past K, and the last codes and scales are read again
-    Codes q;
-    const int k0 = units * kUnit;
-#pragma unroll
-    for (int j = 0; j < kLoads; ++j)
-      x[j] = k0 + 8 * (tid % kPieces) < p.K ? *reinterpret_cast<const u32x4*>(x_ptr[j] + k0) : u32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int piece = (lane % 8) ^ (4 * h + lane / 16);
-        const uint32_t off = k0 / 2 + 16 * piece < p.K / 2 ? uint32_t(k0 / 2) + w_off[t][h] : w_off[t][h] - 16 * piece;
-        q[t][h] = *reinterpret_cast<const u32x4*>((of_up(t) ? w_base[1] : w_base[0]) + off);
-      }
-    const int buf = units & 1;
-    if (units % kChunkUnits == 0) put_scales(chunk);
-    put_x(buf, x);
     put_w(q);
-    take_scales(units, us, ub);
-    __syncthreads();
+    take_scales(at, us, ub);
+    __builtin_amdgcn_sched_barrier(0);
+    load_w(at + 2 < units ? at + 2 : units - 1, q);
+    __builtin_amdgcn_sched_barrier(0);
     both_steps(buf, us, ub);
+    if (kHow == Bias::kMfma && (at % kBlockUnits == kBlockUnits - 1 || at + 1 == units)) {
+      use_biases(at);
+      get_biases(at + 1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    // the buffer was last read a unit ago, which every wave has left
+    if (at + 1 < units) put_x(at + 1, x);
+    __syncthreads();
+  };
+  int at = 0;
+#pragma clang loop unroll(disable)
+  for (; at + 1 < units; at += 2) {
+    turn(at, 0, q0);
+    turn(at + 1, 1, q1);
   }
-
+  if (at < units) turn(at, 0, q0);
   // lane (n, g) holds rows 4 g .. 4 g + 3 of column n of each 16 x 16 tile
 #pragma unroll
   for (int i = 0; i < NB; ++i)
@@ -642,7 +697,10 @@ Shape shape_of(const Int4Product& g) {
   s.direct = s.nb == 1 && g.n_rows <= kDirectRows;
   const int64_t tiles = most_tiles(g.n_rows, g.n_experts, 16 * s.nb);
   const auto groups = [&](int kt, int waves) { return (g.n_dim + (g.w_up ? 8 : 16) * kt * waves - 1) / ((g.w_up ? 8 : 16) * kt * waves); };
-  s.form = tiles * groups(kWideT, 4) >= kManyBlocks ? Form::kWide
+  const bool whole_rows = g.k_dim % kUnit == 0 && g.k_dim / g.group * (g.scales_bf16 ? 2 : 4) % 16 == 0 &&
+                          !((reinterpret_cast<uintptr_t>(g.w_scales) | reinterpret_cast<uintptr_t>(g.w_biases) |
+                             reinterpret_cast<uintptr_t>(g.w_up_scales) | reinterpret_cast<uintptr_t>(g.w_up_biases)) & 15);
+  s.form = whole_rows && tiles * groups(kWideT, 4) >= kManyBlocks ? Form::kWide
            : s.nb == 1 && tiles * groups(4, 1) <= kFewBlocks ? Form::kDeep : Form::kSplitK;
   s.col_groups = int(s.form == Form::kWide ? groups(kWideT, 4) : groups(s.form == Form::kDeep ? 2 : 4, 1));
   s.blocks = tiles * s.col_groups;
