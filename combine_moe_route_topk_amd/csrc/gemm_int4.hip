@@ -91,8 +91,10 @@ __device__ __forceinline__ float row_step(float v) {
 __device__ __forceinline__ float piece_sum(u32x4 x) {
   float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, x[i]), __builtin_bit_cast(bf16x2, 0x3f803f80u), sum, false);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t v = x[i];           // a copy: of an element itself the cast takes element 0
+    sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, v), __builtin_bit_cast(bf16x2, 0x3f803f80u), sum, false);
+  }
   return sum;
 }
 

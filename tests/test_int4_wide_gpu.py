@@ -1,0 +1,86 @@
+"""Products with 4-bit integer weights where there are many tiles, so that the waves
+of a workgroup split the columns: each form against float64.
+
+Tolerance, as for the other forms: (528 + 2 groups + 6) 2^-24 of the sum of magnitudes.
+Here a group's sum rounds at most 128 times and once per group when scaled; X, the sum
+of x over a group, at most 12 times and once in its three bf16 terms; their products
+with the biases are exact and added in at most 3 roundings a group: 141 + 4 groups,
+which is less for up to 193 groups.
+"""
+import numpy as np
+import pytest
+import torch
+
+import combine_moe_route_topk_amd as moe
+from tests.gpu_util import to_dev, to_np
+from tests.test_int4_gpu import BF16, F32, FORMS, _bits, _call, _case, _check, _dev
+
+pytestmark = pytest.mark.gpu
+
+# whole rows of scales in both types, and the last 16 groups half there
+K = {32: 1280, 64: 2560, 128: 5120}
+
+
+@pytest.mark.parametrize("group,affine,scale_dtype", FORMS)
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("r,e,n", [(160, 150, 140), (320, 30, 1001)])
+def test_many_tiles(r, e, n, glu, group, affine, scale_dtype):
+    # one expert of several tiles, one of a full one, one of a single row
+    rng = np.random.default_rng(n)
+    ex = rng.integers(3, e, r)
+    ex[rng.permutation(r)[:70]] = 0
+    ex[rng.permutation(np.nonzero(ex)[0])[:17]] = [1] * 16 + [2]
+    case = _case(r, e, K[group], n, group, affine, scale_dtype, glu, experts=ex)
+    out_dtype = BF16 if glu else F32
+    y = _call(case, scale_dtype, out_dtype)
+    _check(y, case, out_dtype)
+    assert np.array_equal(to_np(y), to_np(_call(case, scale_dtype, out_dtype)))
+
+
+@pytest.mark.parametrize("units", [1, 2, 3, 4, 5])
+def test_many_tiles_short_rows(units):
+    for group in (32, 64, 128):
+        if units * 256 % (8 * group):
+            continue
+        case = _case(160, 150, units * 256, 140, group, True, BF16)
+        _check(_call(case, BF16, F32), case, F32)
+
+
+@pytest.mark.parametrize("affine", [False, True])
+def test_scales_that_begin_at_4_bytes(affine):
+    """Scales that are no whole 16 bytes from a line take another form; the same product."""
+    x, ex, w, _ = case = _case(160, 150, 1280, 140, 32, affine, BF16)
+    want = _call(case, BF16, F32)
+
+    def moved(t):
+        if t is None:
+            return None
+        buf = torch.empty(t.numel() + 2, dtype=t.dtype, device=t.device)
+        buf[2:] = t.reshape(-1)
+        return buf[2:].view(t.shape)
+    codes, s, b = _dev(w, BF16)
+    got = moe.moe_gather_gemm_int4(to_dev(_bits(x)), to_dev(ex), codes, moved(s), moved(b), out_dtype=F32)
+    _check(got, case, F32)
+    _check(want, case, F32)
+
+
+@pytest.mark.parametrize("affine", [False, True])
+def test_one_element_reaches_every_column_once(affine):
+    """x is 1 in one place: the result is that weight, exactly (no other term is not 0)."""
+    r, e, k, n = 160, 150, 1280, 140
+    x, ex, w, _ = _case(r, e, k, n, 32, affine, F32 if not affine else BF16)
+    at = (np.arange(r) * 37) % k
+    x = np.zeros((r, k), np.float32)
+    x[np.arange(r), at] = 1.0
+    scale = F32 if not affine else BF16
+    if affine:                                   # both terms and their sum are bf16 numbers times powers of 2
+        w = (w[0], np.full_like(w[1], 0.5), np.round(w[2] * 64) / 4)
+    y = to_np(_call((x, ex, w, None), scale, F32))
+    byte = w[0][ex, :, at // 2]
+    q = np.where((at % 2 == 1)[:, None], byte >> 4, byte & 15).astype(np.float64)
+    s = w[1][ex, :, at // 32].astype(np.float64)
+    want = s * (q - 8) if not affine else s * q + w[2][ex, :, at // 32]
+    if affine:
+        assert np.array_equal(y, want)
+    else:                                        # s (-8) and s q in one fp32 product of exact sums
+        assert np.array_equal(y, (s * (q - 8)).astype(np.float32))
