@@ -4,14 +4,26 @@
 // X[r, grp] the sum of x over the group; or silu(.) * (the same with w_up).
 //
 // Few rows per expert: the weights are most of the bytes, and each is read once
-// per tile of 16 NB rows, straight from memory into registers.  A code becomes a
-// bf16 number without rounding: a byte 0 .. 15 is q 2^-9 as an fp8 number (its
+// per tile of 16 NB rows, in whole lines, and brought into the operands' order by
+// LDS.  Two kernels, both below: stream_kernel splits K over the waves of a
+// workgroup, wide_kernel the columns.  A code becomes a bf16 number without rounding: a byte 0 .. 15 is q 2^-9 as an fp8 number (its
 // subnormals and the binade above go on in equal steps), which one instruction
 // per two codes turns into bf16 times 2^9.  v_mfma_f32_16x16x32_bf16 multiplies:
 // rows of x are its A operand, 16 weight rows the B operand, so a lane holds
 // results of the one weight row whose codes and scales it reads, and a group's
 // fp32 sum is scaled in fp32.  X comes from the same instruction with a constant
 // for B (-8 where there are no biases, which makes it the sum's start).
+//
+// Measured, bytes of codes, scales and biases over the time:
+//   1024 rows, 256 experts, K 7168, F 2048 SwiGLU, per 128:   671 us, 5.8 TB/s
+//   128 rows, 8 experts, K 4096, F 14336 SwiGLU, per 32 + b:  153 us, 3.8 TB/s
+//   48 rows, 8 experts, K 14336, N 4096, per 64, all fp32:     50 us, 5.3 TB/s
+//   8 rows, 8 of 256 experts, K 2048, N 7168, per 128:         14 us, 4.2 TB/s
+//   1 row, 1 expert, K 7168, N 2113, per 64 + b:               10 us, 0.85 TB/s
+// The first runs at the rate of memory (with the clocks that its power allows; 636
+// us on a cool card), the second at that of the vector units and LDS, which turn 4
+// bits into bf16, scale every 32 elements and serve two row blocks; the last two are
+// one start, a chain of loads and one end, with 29 and 9 KB to read for a workgroup.
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -679,11 +691,22 @@ __global__ __launch_bounds__(256, 2) void wide_kernel(Product p) {
     }
 }
 
-// Mean rows per expert from which a tile holds 32 rows.
+// Mean rows per expert from which a tile holds 32 rows, if there are kManyBlocks such
+// tiles: 8 and 64 experts, K = N = 4096, with tiles of 16 and of 32 rows
+//   16 rows each, at most: 21 and 22 us, 124 and 128 us (of 4: 18 and 35 us)
+//   20 rows each:          28 and 27 us, 171 and 152 us (64: 48 and 40, 317 and 273)
+// and between, where 10 rows are the mean, some experts have more than 16.  One expert
+// of 64, 256 and 512 rows: 11 and 19, 29 and 33 us; K 7168: 75 and 62 us.
 constexpr int64_t kNarrowRows = 10;
-// Workgroups up to which K is split over 8 waves, and a wave has half the columns;
-// from which the waves split the columns.
-constexpr int64_t kFewBlocks = 256, kManyBlocks = 300;
+// Workgroups of 64 columns up to which a workgroup has half of them and splits K over
+// 8 waves instead of 4: up to a workgroup per CU.  One row, K 7168, 128 and 144 of
+// them: 10.6 and 15.7, 17.4 and 16.0 us; K 2048, 64 and 144: 5.6 and 7.1, 9.6 and 7.4.
+constexpr int64_t kFewBlocks = 128;
+// Workgroups of 128 columns from which the waves split the columns.  One row per expert,
+// splitting columns and splitting K: 256 (16 experts, K 4096, N 2048) 16.8 and 17.6 us,
+// 256 (8, K 7168, N 4096) 26.1 and 24.8, 448 (8, K 2048, N 7168) 14.6 and 18.5, 1024
+// (64, K 4096, N 2048) 49.5 and 55.3 us.
+constexpr int64_t kManyBlocks = 300;
 constexpr int kWideT = 2;
 
 enum class Form { kDeep, kSplitK, kWide };
@@ -695,10 +718,11 @@ struct Shape {
 };
 Shape shape_of(const Int4Product& g) {
   Shape s{};
-  s.nb = g.n_rows < kNarrowRows * g.n_experts ? 1 : 2;
+  const auto groups = [&](int kt, int waves) { return (g.n_dim + (g.w_up ? 8 : 16) * kt * waves - 1) / ((g.w_up ? 8 : 16) * kt * waves); };
+  s.nb = g.n_rows < kNarrowRows * g.n_experts ||
+         most_tiles(g.n_rows, g.n_experts, 32) * groups(kWideT, 4) < kManyBlocks ? 1 : 2;
   s.direct = s.nb == 1 && g.n_rows <= kDirectRows;
   const int64_t tiles = most_tiles(g.n_rows, g.n_experts, 16 * s.nb);
-  const auto groups = [&](int kt, int waves) { return (g.n_dim + (g.w_up ? 8 : 16) * kt * waves - 1) / ((g.w_up ? 8 : 16) * kt * waves); };
   const bool whole_rows = g.k_dim % kUnit == 0 && g.k_dim / g.group * (g.scales_bf16 ? 2 : 4) % 16 == 0 &&
                           !((reinterpret_cast<uintptr_t>(g.w_scales) | reinterpret_cast<uintptr_t>(g.w_biases) |
                              reinterpret_cast<uintptr_t>(g.w_up_scales) | reinterpret_cast<uintptr_t>(g.w_up_biases)) & 15);

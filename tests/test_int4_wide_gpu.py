@@ -46,6 +46,13 @@ def test_many_tiles_short_rows(units):
         _check(_call(case, BF16, F32), case, F32)
 
 
+@pytest.mark.parametrize("k", [160, 256, 416, 1056])
+def test_many_rows_and_ends_inside_a_unit(k):
+    for affine, scale_dtype, glu in ((False, BF16, True), (True, F32, False)):
+        case = _case(320, 30, k, 1001, 32, affine, scale_dtype, glu)
+        _check(_call(case, scale_dtype, F32), case, F32)
+
+
 @pytest.mark.parametrize("affine", [False, True])
 def test_scales_that_begin_at_4_bytes(affine):
     """Scales that are no whole 16 bytes from a line take another form; the same product."""
