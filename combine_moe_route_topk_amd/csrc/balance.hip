@@ -13,10 +13,10 @@
 // (a wave four tokens), so the row's maximum and sum are four exchanges within a
 // row of lanes; more experts take a whole wave per token.  A token's logits are
 // asked for while the one before it is worked on.  32768 tokens of 256 experts: 12.9
-// us forward (33.5 MB, 2.6 TB/s) and 8.4 us for the sums, 21.7 us backward (67 MB, 3.1
+// us forward (33.5 MB, 2.6 TB/s) and 8.4 us for the sums, 17.8 us backward (67 MB, 3.8
 // TB/s; a large copy reaches 4.95), with about 25 vector instructions to a logit, two
 // thirds of them the exponential's, which take some 7 us by themselves.  4096 tokens:
-// 4.1, 5.4 and 5.8 us, little more than launches and first loads.
+// 4.1, 5.4 and 5.0 us, little more than launches and first loads.
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -32,7 +32,8 @@ constexpr int kSliceExperts = 32;      // experts per workgroup of the second la
 // Tokens per workgroup, a multiple of the 16 that its waves hold at once, so that
 // about kChunks workgroups share them; up to kOneChunk tokens are one workgroup's,
 // which then finishes the sums itself.  512, 1024 and 2048 for 32768 tokens of 256
-// experts in 37 sequences: 13.9, 13.5 and 13.7 us, backward 24.7, 22.1 and 24.8.
+// experts in 37 sequences: 13.9, 13.5 and 13.7 us, backward (its counts still loaded
+// one by one) 24.7, 22.1 and 24.8.
 constexpr int kChunks = 1024, kOneChunk = 64;
 int64_t chunk_tokens(int64_t n_tokens) {
   const int64_t c = (n_tokens + kChunks - 1) / kChunks;
@@ -426,11 +427,20 @@ __global__ __launch_bounds__(kBlock) void balance_backward_kernel(BackwardArgs a
       const float f = a.d_loss[b] / (float(a.k) * (float(n) * float(n)));
       zf = a.d_z ? 2.f * a.d_z[b] / float(n) : 0.f;
       const double mean = -double(a.k) * double(n);
+      const int32_t* counts = a.counts + int64_t(b) * a.n_experts;
+      // whole numbers below 2^53
+      const auto centred = [&](int c) __attribute__((always_inline)) { return f * float(fma(double(c), double(a.n_experts), mean)); };
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
+      for (int r = 0; r < R; r += 4) {
         const int e = expert_of<LANES>(i, r);
-        // whole numbers below 2^53
-        u[r] = e < a.n_experts ? f * float(fma(double(a.counts[int64_t(b) * a.n_experts + e]), double(a.n_experts), mean)) : 0.f;
+        if (VEC) {
+          const int4 c = e < a.n_experts ? *reinterpret_cast<const int4*>(counts + e) : make_int4(0, 0, 0, 0);
+          u[r] = u[r + 1] = u[r + 2] = u[r + 3] = 0.f;
+          if (e < a.n_experts) { u[r] = centred(c.x); u[r + 1] = centred(c.y); u[r + 2] = centred(c.z); u[r + 3] = centred(c.w); }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) u[r + q] = e + q < a.n_experts ? centred(counts[e + q]) : 0.f;
+        }
       }
     }
     const auto put = [&](int t, const float (&p)[R]) __attribute__((always_inline)) {
@@ -536,7 +546,8 @@ hipError_t launch_balance_loss_backward(const BalanceBackward& g, hipStream_t st
   const BackwardArgs a{g.logits, g.seq_offsets, g.token_mask, g.counts, g.tokens, g.d_loss, g.d_z_loss,
                        int(g.n_tokens), g.n_experts, g.k, g.n_seqs, int(chunk), g.d_logits};
   const unsigned blocks = unsigned((g.n_tokens + chunk - 1) / chunk);
-  const bool vec = rows_of_16_bytes(g.logits, g.n_experts) && rows_of_16_bytes(g.d_logits, g.n_experts);
+  const bool vec = rows_of_16_bytes(g.logits, g.n_experts) && rows_of_16_bytes(g.d_logits, g.n_experts) &&
+                   rows_of_16_bytes(g.counts, g.n_experts);
   by_experts(g.n_experts, vec, [&](auto lanes, auto slots, auto v) {
     constexpr int kL = decltype(lanes)::value, kR = decltype(slots)::value;
     constexpr bool kV = decltype(v)::value;
