@@ -139,26 +139,28 @@ __device__ __forceinline__ void token_softmax(float (&p)[R], float& lse, bool& l
 }
 
 // Runs f(t, v) over the tokens lo + team, + TEAMS, ... before hi that the mask keeps
-// (and g(t) over the others), the next token's logits asked for before f.
+// (and g(t) over the others), the next token's logits asked for before f.  No sum
+// passes hi, which may be the largest int.
 template <int LANES, int R, bool VEC, int TEAMS, typename F, typename G>
 __device__ __forceinline__ void for_tokens(const float* __restrict__ logits, const uint8_t* __restrict__ mask,
-                                           int n_experts, int i, int lo, int hi, F f, G g) {
+                                           int n_experts, int i, int team, int lo, int hi, F f, G g) {
+  if (hi - lo <= team) return;
   float next[R];
   bool keep = false;
   const auto ask = [&](int t) __attribute__((always_inline)) {
-    if (t >= hi) return;
     keep = !mask || mask[t];
     load_token<LANES, R, VEC>(logits + int64_t(t) * n_experts, n_experts, i, next);
   };
-  ask(lo);
-  for (int t = lo; t < hi; t += TEAMS) {
+  ask(lo + team);
+  for (int t = lo + team;; t += TEAMS) {
     float v[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) v[r] = next[r];
-    const bool kept = keep;
-    ask(t + TEAMS);
+    const bool kept = keep, more = hi - t > TEAMS;
+    if (more) ask(t + TEAMS);
     if (kept) f(t, v);
     else g(t);
+    if (!more) break;
   }
 }
 
@@ -254,7 +256,7 @@ __global__ __launch_bounds__(kBlock) void balance_kernel(ForwardArgs a) {
         if (unsigned(e) < unsigned(a.n_experts)) atomicAdd(&s_c[e], 1);
       }
     };
-    for_tokens<LANES, R, VEC, kTeams>(a.logits, a.mask, a.n_experts, i, lo + team, hi, add, [](int) {});
+    for_tokens<LANES, R, VEC, kTeams>(a.logits, a.mask, a.n_experts, i, team, lo, hi, add, [](int) {});
 #pragma unroll
     for (int r = 0; r < R; ++r) s_p[team][expert_of<LANES>(i, r)] = acc[r];
     if (i == 0) { s_z[team] = z; s_n[team] = n; }
@@ -472,10 +474,10 @@ __global__ __launch_bounds__(kBlock) void balance_backward_kernel(BackwardArgs a
       put(t, p);
     };
     if (n <= 0) {
-      for (int t = lo + team; t < hi; t += kTeams) none(t);
+      for (int left = hi - lo - team; left > 0; left -= kTeams) none(hi - left);
       return;
     }
-    for_tokens<LANES, R, VEC, kTeams>(a.logits, a.mask, a.n_experts, i, lo + team, hi,
+    for_tokens<LANES, R, VEC, kTeams>(a.logits, a.mask, a.n_experts, i, team, lo, hi,
                                       [&](int t, float (&p)[R]) __attribute__((always_inline)) {
       float lse, dot = 0.f;
       bool live;

@@ -103,6 +103,22 @@ def test_quantize_ties_and_neighbours(group, affine, scale_dtype):
     _same_quantize(codecs.bf16_bits_to_f32(_bits(x)), BF16, group, affine, scale_dtype)
 
 
+def test_quantize_every_bf16_quotient():
+    """Every mantissa of the largest magnitude, which fixes the scale, and every bf16
+    number from it down to where all codes are 8, both signs, at several exponents."""
+    for group, p in ((32, 0), (64, -40), (128, 90), (128, -99), (128, -101), (128, -121)):
+        rows = []
+        for m in range(128, 256):
+            top = (np.uint32(m - 128) | np.uint32((p + 127) << 7)).astype(np.uint16)
+            low = max(int(top) - 6 * 128, 0)
+            v = np.arange(low, int(top) + 1).astype(np.uint16)
+            v = np.concatenate([v, v | np.uint16(0x8000)])
+            v = np.resize(v, (v.size + group - 2) // (group - 1) * (group - 1)).reshape(-1, group - 1)
+            rows.append(np.concatenate([np.full((len(v), 1), top, np.uint16), v], 1))
+        x = codecs.bf16_bits_to_f32(np.concatenate(rows))
+        _same_quantize(x, BF16, group, False, BF16)
+
+
 def _one(rng, scale_dtype):
     v = np.float32(rng.uniform(1, 2) * 2.0 ** rng.integers(-60, 60))
     return codecs.bf16_bits_to_f32(_bits(v.reshape(1)))[0] if scale_dtype == BF16 else v
