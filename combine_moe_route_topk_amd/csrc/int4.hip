@@ -27,7 +27,8 @@ constexpr int kBlock = 256;
 // Octets per thread, and the size from which x is loaded past the last-level cache
 // (256 MB).  Measured on 114688 x 4096 bf16, groups of 128, quantising with 1, 2 and
 // 4 octets: 237, 189 and 193 us (1.18 GB, 6.2 TB/s); back to bf16 with 1, 2, 4 and 8:
-// 226, 161, 165 and 166 (7.2 TB/s).  With ordinary loads quantising takes 222 us.
+// 226, 161, 165 and 166 (7.2 TB/s).  With ordinary loads quantising took 222 us.  (The
+// rounding below then took more instructions; with 2 octets it is 181 us now, 6.5 TB/s.)
 // 2113 x 7168 fp32 with biases per 32: 13.2 and 7.8 us (the launches and the groups'
 // exchanges; 71 MB of x would take 9).
 constexpr int kQuant = 2, kDequant = 4;
@@ -141,9 +142,12 @@ constexpr float kNearHalf = 0.5f - 0x1p-16f;
 // Of bf16 x and s no slow path is needed: with mantissas of 8 bits a quotient of at
 // least 1/4 that is no half is 2^-11 or more away from every half, so x (1 / s)
 // rounded to multiples of 2^-12, which the sum with 2^11 does, is a half when x / s is
-// one and on the same side of it when not.  Ties are common there (3 waves of 8 held
-// one): 128 x 7168 x 512 bf16 takes 192 us so and 265 with the remainders.
-constexpr float kGrid = 0x1p+11f;
+// one and on the same side of it when not.  2^23 more rounds that to a whole number,
+// ties to even, in the sum's low bits, which are added up as integers.  Ties are common
+// there (3 waves of 8 held one): 114688 x 4096 bf16 takes 181 us so, 188 with the
+// codes taken from floats and 265 with the remainders.
+constexpr float kGrid = 0x1p+11f, kWhole = 0x1p+23f;
+constexpr uint32_t kWholeBits = 0x4b000800u;   // of 2^23 + 2^11
 
 // The codes and, in the first lane of each group, the scale (and bias) of an octet.
 template <int GROUP, bool AFFINE, typename T, typename S>
@@ -174,14 +178,22 @@ __device__ __forceinline__ void quantize_octet(const Octet<T>& x, int64_t g, uin
     bu *= 0x1p+64f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= 0x1p+64f;
+    // elsewhere a symmetric quotient is at most 7 (1 + 2^-8); one whose scale is below
+    // the normal numbers may be larger, and is clamped here, off every half
+    if (!AFFINE) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], -8.25f * su), 7.25f * su);
+    }
   }
   const float inv = su > 0.f ? __builtin_amdgcn_rcpf(su) : 0.f;
-  float q[8];
-  if (!AFFINE && sizeof(T) == 2 && sizeof(S) == 2) {
+  uint32_t packed;
+  if constexpr (!AFFINE && sizeof(T) == 2 && sizeof(S) == 2) {
+    packed = 0u - kWholeBits * 0x11111111u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = rintf(fmaf(v[i], inv, kZero + kGrid) - kGrid);
+    for (int i = 0; i < 8; ++i)
+      packed += __float_as_uint(fmaf(v[i], inv, kZero + kGrid) + kWhole) << (4 * i);
   } else {
-    float far = 0.f;
+    float q[8], far = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float w = fmaf(AFFINE ? v[i] - bu : v[i], inv, kZero);
@@ -205,10 +217,11 @@ __device__ __forceinline__ void quantize_octet(const Octet<T>& x, int64_t g, uin
         q[i] += (over > 0.f) | ((over == 0.f) & odd) ? up : 0.f;
       }
     }
-  }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = fminf(fmaxf(q[i], 0.f), 15.f);
-  codes[g] = bad ? (AFFINE ? 0u : 0x88888888u) : pack8(q);
+    for (int i = 0; i < 8; ++i) q[i] = fminf(fmaxf(q[i], 0.f), 15.f);
+    packed = pack8(q);
+  }
+  codes[g] = bad ? (AFFINE ? 0u : 0x88888888u) : packed;
   if (g % (GROUP / 8) == 0) {
     const float nan = __uint_as_float(0x7fc00000u);
     put_scale(scales, g / (GROUP / 8), bad ? nan : s);
