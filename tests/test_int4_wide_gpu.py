@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import combine_moe_route_topk_amd as moe
-from tests.gpu_util import to_dev, to_np
+from tests.gpu_util import DEV, to_dev, to_np
 from tests.test_int4_gpu import BF16, F32, FORMS, _bits, _call, _case, _check, _dev
 
 pytestmark = pytest.mark.gpu
@@ -91,3 +91,65 @@ def test_one_element_reaches_every_column_once(affine):
         assert np.array_equal(y, want)
     else:                                        # s (-8) and s q in one fp32 product of exact sums
         assert np.array_equal(y, (s * (q - 8)).astype(np.float32))
+
+
+@pytest.mark.parametrize("r,e,n", [(160, 150, 140), (320, 30, 1001)])
+def test_many_tiles_rows_without_an_expert_stay(r, e, n):
+    ex = np.arange(r) % e
+    ex[::4], ex[1::5], ex[2::7] = -1, e, -2**31
+    case = _case(r, e, 1280, n, 32, True, BF16, experts=ex)
+    y = torch.full((r, n), 7.0, dtype=F32, device=DEV)
+    _call(case, BF16, F32, y=y)
+    _check(y, case, F32)
+    assert (y[to_dev((ex < 0) | (ex >= e))] == 7).all()
+
+
+@pytest.mark.parametrize("affine", [False, True])
+@pytest.mark.parametrize("r,e,n", [(160, 150, 140), (320, 30, 1001)])
+def test_many_tiles_nan_and_infinity_stay(r, e, n, affine):
+    case = _case(r, e, 1280, n, 32, affine, BF16, experts=np.arange(r) % e)
+    clean = _call(case, BF16, F32)
+    x = case[0].copy()
+    x[2, 3], x[5, 1279] = np.nan, np.inf
+    got = _call((x, *case[1:]), BF16, F32)
+    rows = torch.ones(r, dtype=torch.bool, device=DEV)
+    rows[[2, 5]] = False
+    assert not torch.isfinite(got[~rows]).any() and torch.equal(got[rows], clean[rows])
+    hit = torch.zeros((r, n), dtype=torch.bool, device=DEV)
+    hit[to_dev(case[1] == 0), 7] = True
+    for part in (1, 2) if affine else (1,):            # a scale, a bias
+        w = [v if v is None else v.copy() for v in case[2]]
+        w[part][0, 7, -1] = np.nan
+        got = _call((case[0], case[1], tuple(w), None), BF16, F32)
+        assert torch.isnan(got[hit]).all() and torch.equal(got[~hit], clean[~hit])
+
+
+def test_many_tiles_replayed():
+    """Two captured products, of 16- and 32-row tiles, that share a workspace."""
+    ws = torch.empty(max(moe.moe_gather_gemm_int4_workspace_bytes(r, e) for r, e in ((160, 150), (320, 30))),
+                     dtype=torch.uint8, device=DEV)
+    steps = []
+    for r, e, n in ((160, 150, 140), (320, 30, 1001)):
+        case = _case(r, e, 1280, n, 32, True, BF16)
+        w, x, ex = _dev(case[2], BF16), to_dev(_bits(case[0])), to_dev(case[1])
+        y = torch.empty((r, n), dtype=BF16, device=DEV)
+
+        def step(x=x, ex=ex, w=w, y=y):
+            moe.moe_gather_gemm_int4(x, ex, *w, y=y, workspace=ws)
+        step()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        steps.append((x, ex, e, y, step, g))
+    for rep in range(4):
+        for x, ex, e, y, step, g in steps:
+            x.copy_(torch.roll(x, 1, 0))
+            ex.copy_((ex + 1) % e)
+            y.fill_(7)
+            ws.fill_(255)
+            g.replay()
+            got = y.clone()
+            torch.cuda.synchronize()
+            step()
+            assert torch.equal(got, y), rep
