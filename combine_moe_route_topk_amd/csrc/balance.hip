@@ -29,15 +29,21 @@ namespace {
 constexpr int kBlock = 256;
 constexpr int kSliceExperts = 32;      // experts per workgroup of the second launch
 
-// Tokens per workgroup, a multiple of the 16 that its waves hold at once, so that
+// Tokens per workgroup, usually a multiple of the 16 that its waves hold at once, so that
 // about kChunks workgroups share them; up to kOneChunk tokens are one workgroup's,
 // which then finishes the sums itself.  512, 1024 and 2048 for 32768 tokens of 256
 // experts in 37 sequences: 13.9, 13.5 and 13.7 us, backward (its counts still loaded
 // one by one) 24.7, 22.1 and 24.8.
-constexpr int kChunks = 1024, kOneChunk = 64;
-int64_t chunk_tokens(int64_t n_tokens) {
-  const int64_t c = (n_tokens + kChunks - 1) / kChunks;
-  return c < 16 ? 16 : (c + 15) / 16 * 16;
+// Sequences follow one another within a chunk, each with its own chain of loads, so
+// a chunk holds no more tokens than a sequence does on average, and one workgroup
+// takes all tokens of at most kOneSeqs sequences.  256 experts, 12 tokens in 44
+// sequences 29 -> 13 us and backward 28 -> 5, 51 in 16: 31 -> 14 and 13 -> 9; 64 tokens
+// in 3 and 4, one workgroup or two launches: 10.5 and 10.8, 12.6 and 11.0 us.
+constexpr int kChunks = 1024, kOneChunk = 64, kOneSeqs = 3;
+int64_t chunk_tokens(int64_t n_tokens, int64_t n_seqs) {
+  const int64_t c = (n_tokens + kChunks - 1) / kChunks, mean = n_tokens / n_seqs;
+  const int64_t most = c < 16 ? 16 : (c + 15) / 16 * 16;
+  return mean < 1 ? 1 : (mean < most ? mean : most);
 }
 
 // Sums of one sequence within one chunk of tokens.  Chunk c and sequence b meet
@@ -58,7 +64,7 @@ struct Layout {
 };
 Layout layout_of(int64_t n_tokens, int n_experts, int64_t n_seqs) {
   Layout L{};
-  L.chunk = chunk_tokens(n_tokens);
+  L.chunk = chunk_tokens(n_tokens, n_seqs);
   L.chunks = (n_tokens + L.chunk - 1) / L.chunk;
   L.slots = L.chunks + n_seqs;
   L.slices = (n_experts + kSliceExperts - 1) / kSliceExperts;
@@ -525,7 +531,7 @@ hipError_t launch_balance_loss(const BalanceForward& g, void* workspace, hipStre
   const Partials part{reinterpret_cast<float*>(ws), reinterpret_cast<int32_t*>(ws + L.counts),
                       reinterpret_cast<int32_t*>(ws + L.tokens), reinterpret_cast<float*>(ws + L.z),
                       reinterpret_cast<int32_t*>(ws + L.tickets), reinterpret_cast<float*>(ws + L.slice_sums)};
-  const bool one = g.n_tokens <= kOneChunk && int64_t(g.n_seqs) * g.n_experts <= 65536;
+  const bool one = g.n_tokens <= kOneChunk && g.n_seqs <= kOneSeqs;
   const ForwardArgs a{g.logits, g.topk_idx, g.seq_offsets, g.token_mask, int(g.n_tokens), g.n_experts, g.k,
                       g.n_seqs, one ? kOneChunk : int(L.chunk), g.loss, g.z_loss, g.counts, g.probs, g.tokens, part};
   by_experts(g.n_experts, rows_of_16_bytes(g.logits, g.n_experts), [&](auto lanes, auto slots, auto vec) {
@@ -544,7 +550,7 @@ hipError_t launch_balance_loss(const BalanceForward& g, void* workspace, hipStre
 }
 
 hipError_t launch_balance_loss_backward(const BalanceBackward& g, hipStream_t stream) {
-  const int64_t chunk = chunk_tokens(g.n_tokens);
+  const int64_t chunk = chunk_tokens(g.n_tokens, g.n_seqs);
   const BackwardArgs a{g.logits, g.seq_offsets, g.token_mask, g.counts, g.tokens, g.d_loss, g.d_z_loss,
                        int(g.n_tokens), g.n_experts, g.k, g.n_seqs, int(chunk), g.d_logits};
   const unsigned blocks = unsigned((g.n_tokens + chunk - 1) / chunk);
