@@ -312,84 +312,98 @@ __global__ __launch_bounds__(kBlock) void balance_kernel(ForwardArgs a) {
 // thread are in flight, and the last workgroup asks for all parts at once: 256 slots
 // of 256 experts 10.5 -> 5.4 us, of which the ticket and its visibility are about 3.
 constexpr int kDeep = 8;
-template <bool VEC>
+// LOOP: a workgroup per sequence takes all its experts, 32 after 32, and draws no
+// ticket, from kLoopBlocks workgroups of the other form on (each ticket makes a cache
+// visible to the other XCDs).  The whole loss of 4096 tokens of 256 experts in 64, 128
+// and 512 sequences, with tickets 21, 30 and 86 us, without 24, 25 and 27.
+constexpr int64_t kLoopBlocks = 768;
+template <bool VEC, bool LOOP>
 __global__ __launch_bounds__(kBlock) void balance_sum_kernel(ForwardArgs a, int n_slices) {
   constexpr int kQuads = kSliceExperts / 4, kRows = kBlock / kQuads;
   __shared__ float s_p[kRows][kSliceExperts + 1];
   __shared__ int s_c[kRows][kSliceExperts + 1];
   __shared__ float s_z[kBlock];
   __shared__ int s_n[kBlock];
-  const int b = blockIdx.x / n_slices, slice = blockIdx.x % n_slices;
+  const int b = LOOP ? blockIdx.x : blockIdx.x / n_slices;
+  int slice = LOOP ? 0 : blockIdx.x % n_slices;
   const int tid = threadIdx.x, q = tid % kQuads, row = tid / kQuads;
   int lo = a.offs ? a.offs[b] : 0, hi = a.offs ? a.offs[b + 1] : a.n_tokens;
   lo = lo < 0 ? 0 : (lo > a.n_tokens ? a.n_tokens : lo);
   hi = hi < lo ? lo : (hi > a.n_tokens ? a.n_tokens : hi);
   const int64_t first = int64_t(lo / a.chunk) + b;
   const int count = hi > lo ? (hi - 1) / a.chunk - lo / a.chunk + 1 : 0;
-  const int e0 = slice * kSliceExperts + 4 * q;
 
-  float p[4] = {0.f, 0.f, 0.f, 0.f};
-  int c[4] = {0, 0, 0, 0};
-  for (int s = row; s < count; s += kDeep * kRows) {
-    float pr[kDeep][4];
-    int cr[kDeep][4];
-#pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
-      const int at_row = s + d * kRows;
-      const int64_t at = (first + (at_row < count ? at_row : s)) * a.n_experts + e0;
-      if (VEC) {
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        int4 y = make_int4(0, 0, 0, 0);
-        if (e0 < a.n_experts) {
-          x = *reinterpret_cast<const float4*>(a.part.probs + at);
-          y = *reinterpret_cast<const int4*>(a.part.counts + at);
-        }
-        pr[d][0] = x.x; pr[d][1] = x.y; pr[d][2] = x.z; pr[d][3] = x.w;
-        cr[d][0] = y.x; cr[d][1] = y.y; cr[d][2] = y.z; cr[d][3] = y.w;
-      } else {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          pr[d][v] = e0 + v < a.n_experts ? a.part.probs[at + v] : 0.f;
-          cr[d][v] = e0 + v < a.n_experts ? a.part.counts[at + v] : 0;
-        }
-      }
-    }
-#pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
-      if (s + d * kRows >= count) break;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) { p[v] += pr[d][v]; c[v] += cr[d][v]; }
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < 4; ++v) { s_p[row][4 * q + v] = p[v]; s_c[row][4 * q + v] = c[v]; }
-  float z = 0.f;
+  float z = 0.f, dot = 0.f, part = 0.f;          // part: in lane s, of slice s
   int n = 0;
   for (int s = tid; s < count; s += kBlock) { z += a.part.z[first + s]; n += a.part.tokens[first + s]; }
   s_z[tid] = z;
   s_n[tid] = n;
-  __syncthreads();
-  if (tid >= kWave) return;
-
-  // one wave is left: its lanes add the tokens, and 32 of them an expert each
-  z = 0.f;
-  n = 0;
-  for (int w = 0; w < kBlock; w += kWave) { z += s_z[w + tid]; n += s_n[w + tid]; }
-  z = reduce_lanes<kWave>(z, Add());
-  for (int d = 1; d < kWave; d <<= 1) n += __shfl_xor(n, d);
-  float dot = 0.f;
-  const int e = slice * kSliceExperts + tid;
-  if (tid < kSliceExperts && e < a.n_experts) {
-    float sum = 0.f;
-    int cs = 0;
+  for (;; ++slice) {
+    const int e0 = slice * kSliceExperts + 4 * q;
+    float p[4] = {0.f, 0.f, 0.f, 0.f};
+    int c[4] = {0, 0, 0, 0};
+    for (int s = row; s < count; s += kDeep * kRows) {
+      float pr[kDeep][4];
+      int cr[kDeep][4];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) { sum += s_p[r][tid]; cs += s_c[r][tid]; }
-    a.counts[int64_t(b) * a.n_experts + e] = cs;
-    a.probs[int64_t(b) * a.n_experts + e] = n > 0 ? sum / float(n) : 0.f;
-    dot = float(cs) * sum;
+      for (int d = 0; d < kDeep; ++d) {
+        const int at_row = s + d * kRows;
+        const int64_t at = (first + (at_row < count ? at_row : s)) * a.n_experts + e0;
+        if (VEC) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          int4 y = make_int4(0, 0, 0, 0);
+          if (e0 < a.n_experts) {
+            x = *reinterpret_cast<const float4*>(a.part.probs + at);
+            y = *reinterpret_cast<const int4*>(a.part.counts + at);
+          }
+          pr[d][0] = x.x; pr[d][1] = x.y; pr[d][2] = x.z; pr[d][3] = x.w;
+          cr[d][0] = y.x; cr[d][1] = y.y; cr[d][2] = y.z; cr[d][3] = y.w;
+        } else {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            pr[d][v] = e0 + v < a.n_experts ? a.part.probs[at + v] : 0.f;
+            cr[d][v] = e0 + v < a.n_experts ? a.part.counts[at + v] : 0;
+          }
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < kDeep; ++d) {
+        if (s + d * kRows >= count) break;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) { p[v] += pr[d][v]; c[v] += cr[d][v]; }
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) { s_p[row][4 * q + v] = p[v]; s_c[row][4 * q + v] = c[v]; }
+    __syncthreads();
+    if (tid < kWave) {
+      // its lanes add the tokens, and 32 of them an expert each
+      z = 0.f;
+      n = 0;
+      for (int w = 0; w < kBlock; w += kWave) { z += s_z[w + tid]; n += s_n[w + tid]; }
+      z = reduce_lanes<kWave>(z, Add());
+      for (int d = 1; d < kWave; d <<= 1) n += __shfl_xor(n, d);
+      dot = 0.f;
+      const int e = slice * kSliceExperts + tid;
+      if (tid < kSliceExperts && e < a.n_experts) {
+        float sum = 0.f;
+        int cs = 0;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) { sum += s_p[r][tid]; cs += s_c[r][tid]; }
+        a.counts[int64_t(b) * a.n_experts + e] = cs;
+        a.probs[int64_t(b) * a.n_experts + e] = n > 0 ? sum / float(n) : 0.f;
+        dot = float(cs) * sum;
+      }
+      dot = reduce_lanes<kWave>(dot, Add());
+      if (LOOP && tid == slice) part = dot;
+    }
+    if (!LOOP || slice + 1 == n_slices) break;
+    __syncthreads();                             // s_p and s_c are read
   }
-  dot = reduce_lanes<kWave>(dot, Add());
-  if (n_slices > 1) {
+  if (tid >= kWave) return;
+  if (LOOP) {
+    dot = reduce_lanes<kWave>(part, Add());
+  } else if (n_slices > 1) {
     float* parts = a.part.slices + int64_t(b) * n_slices;
     int last = 0;
     if (tid == 0) {
@@ -542,9 +556,15 @@ hipError_t launch_balance_loss(const BalanceForward& g, void* workspace, hipStre
     else balance_kernel<kL, kR, kV, false><<<L.chunks > 0 ? unsigned(L.chunks) : 1u, kBlock, 0, stream>>>(a);
   });
   if (!one) {
-    const unsigned blocks = unsigned(g.n_seqs) * unsigned(L.slices);
-    if (g.n_experts % 4 == 0) balance_sum_kernel<true><<<blocks, kBlock, 0, stream>>>(a, L.slices);
-    else balance_sum_kernel<false><<<blocks, kBlock, 0, stream>>>(a, L.slices);
+    const bool loop = int64_t(g.n_seqs) * L.slices >= kLoopBlocks;
+    const unsigned blocks = unsigned(g.n_seqs) * unsigned(loop ? 1 : L.slices);
+    const auto sum = [&](auto vec) {
+      constexpr bool kV = decltype(vec)::value;
+      if (loop) balance_sum_kernel<kV, true><<<blocks, kBlock, 0, stream>>>(a, L.slices);
+      else balance_sum_kernel<kV, false><<<blocks, kBlock, 0, stream>>>(a, L.slices);
+    };
+    if (g.n_experts % 4 == 0) sum(std::true_type());
+    else sum(std::false_type());
   }
   return hipGetLastError();
 }
