@@ -802,6 +802,8 @@ def _balance_tokens(fn, logits, seq_offsets, token_mask):
 
 @functools.lru_cache(maxsize=1024)        # a function of the sizes alone
 def moe_balance_loss_workspace_bytes(n_tokens: int, n_experts: int, n_sequences: int = 1) -> int:
+    """Bytes of moe_balance_loss's workspace, no less for more tokens, experts or sequences:
+    one made for the largest batch holds every smaller one."""
     return int(lib.moe_balance_loss_workspace_bytes(n_tokens, n_experts, n_sequences))
 
 

@@ -57,8 +57,19 @@ struct Partials {
   int32_t* tickets;    // [B]
   float* slices;       // [B, slices]: parts of a sequence's loss
 };
+// Slots of a call, or more: the most that n <= n_tokens tokens in b <= n_seqs sequences
+// take, so that a workspace made for the largest batch holds every smaller one.  Fewer
+// tokens can take more chunks, since a chunk's length jumps.  Where it is the 16 ceil(n /
+// 16384) tokens of chunk_tokens there are at most n / 16 chunks and at most 1024; where it
+// is the mean m = n / b >= 1, ceil(n / m) <= b + ceil((b - 1) / m) <= 2 b - 1; with m < 1
+// they are n < b; and n at most in every case.
+int64_t most_slots(int64_t n_tokens, int64_t n_seqs) {
+  const int64_t even = (n_tokens + 15) / 16 < kChunks ? (n_tokens + 15) / 16 : kChunks;
+  const int64_t by_mean = n_tokens < 2 * n_seqs - 1 ? n_tokens : 2 * n_seqs - 1;
+  return (even > by_mean ? even : by_mean) + n_seqs;
+}
 struct Layout {
-  int64_t chunk, chunks, slots;
+  int64_t chunk, chunks;
   int slices;
   size_t counts, tokens, z, tickets, slice_sums, total;
 };
@@ -66,13 +77,13 @@ Layout layout_of(int64_t n_tokens, int n_experts, int64_t n_seqs) {
   Layout L{};
   L.chunk = chunk_tokens(n_tokens, n_seqs);
   L.chunks = (n_tokens + L.chunk - 1) / L.chunk;
-  L.slots = L.chunks + n_seqs;
+  const int64_t slots = most_slots(n_tokens, n_seqs);
   L.slices = (n_experts + kSliceExperts - 1) / kSliceExperts;
   const auto after = [](size_t o, size_t n) { return (o + n * 4 + 255) / 256 * 256; };
-  L.counts = after(0, size_t(L.slots) * n_experts);
-  L.tokens = after(L.counts, size_t(L.slots) * n_experts);
-  L.z = after(L.tokens, size_t(L.slots));
-  L.tickets = after(L.z, size_t(L.slots));
+  L.counts = after(0, size_t(slots) * n_experts);
+  L.tokens = after(L.counts, size_t(slots) * n_experts);
+  L.z = after(L.tokens, size_t(slots));
+  L.tickets = after(L.z, size_t(slots));
   L.slice_sums = after(L.tickets, size_t(n_seqs));
   L.total = after(L.slice_sums, size_t(n_seqs) * L.slices);
   return L;

@@ -586,7 +586,8 @@ int moe_gather_gemm_mxfp4(const uint8_t* rows, const uint8_t* row_scales, int64_
  * fp32 sums in a fixed order: the same inputs give the same bits.
  *
  * moe_balance_loss_workspace_bytes -- workspace of moe_balance_loss; 0 for
- * invalid sizes. */
+ * invalid sizes.  No less for more tokens, experts or sequences: a workspace for
+ * the largest batch holds every smaller one. */
 size_t moe_balance_loss_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t n_sequences);
 
 /* moe_balance_loss
