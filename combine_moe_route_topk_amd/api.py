@@ -746,6 +746,7 @@ def moe_grouped_gemm_mxfp4(rows: torch.Tensor, row_scales: torch.Tensor,
 
 @functools.lru_cache(maxsize=1024)        # a function of the sizes alone
 def moe_gather_gemm_mxfp4_workspace_bytes(n_rows: int, n_experts: int) -> int:
+    """Bytes of moe_gather_gemm_mxfp4's workspace, no less for more rows or experts."""
     return int(lib.moe_gather_gemm_mxfp4_workspace_bytes(n_rows, n_experts))
 
 
@@ -967,6 +968,7 @@ def moe_dequant_int4(codes: torch.Tensor, scales: torch.Tensor, biases: Optional
 
 @functools.lru_cache(maxsize=1024)        # a function of the sizes alone
 def moe_gather_gemm_int4_workspace_bytes(n_rows: int, n_experts: int) -> int:
+    """Bytes of moe_gather_gemm_int4's workspace, no less for more rows or experts."""
     return int(lib.moe_gather_gemm_int4_workspace_bytes(n_rows, n_experts))
 
 

@@ -135,7 +135,8 @@ __device__ __forceinline__ Tile direct_tile(int m, const int32_t* __restrict__ r
   return t;
 }
 
-// Workspace of the gather form: the maps of a sorted dispatch of the ids.
+// Workspace of the gather form: the maps of a sorted dispatch of the ids.  It grows
+// with rows and experts, so that one made for the most rows holds every smaller call.
 struct GatherLayout {
   size_t counts, offsets, seg_offsets, dst_pos, order, dispatch_ws, total;
 };
@@ -148,7 +149,7 @@ GatherLayout gather_layout(int64_t n_rows, int n_experts) {
   L.seg_offsets = o; o += round256(2 * 4);
   L.dst_pos = o;     o += round256(size_t(n_rows) * 4);
   L.order = o;       o += round256(size_t(n_rows) * 4);
-  L.dispatch_ws = o; o += round256(dispatch_workspace_bytes(n_rows, n_experts, 1, 1));
+  L.dispatch_ws = o; o += round256(dispatch_workspace_bytes_up_to(n_rows, n_experts));
   L.total = o;
   return L;
 }

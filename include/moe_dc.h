@@ -550,7 +550,7 @@ int moe_grouped_gemm_mxfp4(const uint8_t* rows, const uint8_t* row_scales, int64
                            const uint8_t* w_up_scales, int64_t n_dim, void* y, void* stream);
 
 /* moe_gather_gemm_mxfp4_workspace_bytes -- workspace of moe_gather_gemm_mxfp4.
- * 0 for invalid sizes. */
+ * 0 for invalid sizes; no less for more rows or experts. */
 size_t moe_gather_gemm_mxfp4_workspace_bytes(int64_t n_rows, int32_t n_experts);
 
 /* moe_gather_gemm_mxfp4 -- the product of moe_grouped_gemm_mxfp4 over rows left
@@ -660,7 +660,7 @@ int moe_dequant_int4(const uint8_t* codes, const void* scales, const void* biase
                      void* stream);
 
 /* moe_gather_gemm_int4_workspace_bytes -- workspace of moe_gather_gemm_int4.
- * 0 for invalid sizes. */
+ * 0 for invalid sizes; no less for more rows or experts. */
 size_t moe_gather_gemm_int4_workspace_bytes(int64_t n_rows, int32_t n_experts);
 
 /* moe_gather_gemm_int4 -- expert products with 4-bit integer weights over bf16
