@@ -51,7 +51,7 @@ struct Product {
   const uint16_t* rows;
   int n_rows, K;
   const int32_t* index;                // expert offsets, or with direct the expert of each row
-  const int32_t* order;                // row of each grouped position, or null
+  const int32_t* order;                // row of each grouped position (null with direct)
   int n_experts, N;
   const uint8_t* w[2];                 // w and w_up
   const void* s[2];
@@ -193,7 +193,7 @@ __global__ __launch_bounds__(WAVES * kWave, (NB == 1 && (kScaleBytes<G, S, BIAS>
   if (!tile.valid) return;             // whole workgroup
   // rows of the tile (row_end is the expert's); past them its first is read, and never stored
   const int live = tile.row_end - tile.row0 < kTM ? tile.row_end - tile.row0 : kTM;
-  if (!p.direct && tid < live) s_rows[tid] = p.order ? p.order[tile.row0 + tid] : tile.row0 + tid;
+  if (!p.direct && tid < live) s_rows[tid] = p.order[tile.row0 + tid];
   __syncthreads();
 
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -447,7 +447,7 @@ __global__ __launch_bounds__(256, 2) void wide_kernel(Product p) {
   if (!tile.valid) return;             // whole workgroup
   // rows of the tile (row_end is the expert's); past them its first is read, and never stored
   const int live = tile.row_end - tile.row0 < kTM ? tile.row_end - tile.row0 : kTM;
-  if (!p.direct && tid < live) s_rows[tid] = p.order ? p.order[tile.row0 + tid] : tile.row0 + tid;
+  if (!p.direct && tid < live) s_rows[tid] = p.order[tile.row0 + tid];
   if constexpr (kHow == Bias::kMfma) {         // groups past K are multiplied by 0
     uint16_t* sums = &s_sums[0][0][0][0];
     for (int i = tid; i < 2 * 3 * kTM * 16; i += kThreads) sums[i] = 0;
