@@ -135,8 +135,10 @@ __device__ __forceinline__ uint32_t pack8(const float (&q)[8]) {
 }
 
 // Past this distance from the nearest integer, x (1 / s) may be on the other side
-// of a half than x / s: the quotient is within 16 in magnitude, the reciprocal,
-// the product and the difference x - b err by 2^-24 or so each, relatively.
+// of a half than x / s: for a quotient within 16 in magnitude, since the reciprocal,
+// the product and the difference x - b err by 2^-24 or so each, relatively.  Larger
+// ones, of either sign, come up where a bf16 bias is far from the group's minimum for
+// its range; they are clamped to 0 or 15 whichever way they are rounded.
 constexpr float kNearHalf = 0.5f - 0x1p-16f;
 
 // Of bf16 x and s no slow path is needed: with mantissas of 8 bits a quotient of at
