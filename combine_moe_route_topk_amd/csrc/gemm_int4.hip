@@ -42,8 +42,11 @@ constexpr int kStep = 128;             // elements of K that one 16-byte load pe
 constexpr int kUnit = 256;             // elements of K asked for together: whole lines of a weight row
 
 // Bytes of scales and biases of a weight row in a unit.  They share the registers
-// with the codes: from some number on (where the compiler would spill) a SIMD holds
-// one wave of a kernel.
+// with the codes: past 16, a SIMD holds one wave of a kernel whose tiles have 16 rows.
+// Two waves keep at most 24 registers in memory at 16 bytes (4 to 24, and none below),
+// and 72 to 212 past them.  One wave and two, 1024 rows over 128 experts, K 1408, N 2048:
+// at 16 bytes (per 64 with bf16 biases) 161 and 103 us, at 32 (per 64, fp32 with biases)
+// 163 and 219; 16 rows over 16 experts, K 4096, N 1024: 13.9 and 14.5, 14.9 and 34 us.
 template <int G, typename S, bool BIAS>
 constexpr int kScaleBytes = (BIAS ? 2 : 1) * int(sizeof(S)) * kUnit / G;
 
