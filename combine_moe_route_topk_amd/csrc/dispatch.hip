@@ -706,15 +706,6 @@ size_t dispatch_workspace_bytes(int64_t n_tokens, int n_experts, int k, int n_se
   return cells * sizeof(int32_t) + 256;
 }
 
-size_t dispatch_workspace_bytes_up_to(int64_t n_pairs, int n_experts) {
-  // at most 64 chunks of 256 pairs or more up to 65536 pairs, then 1024 pairs each up to
-  // 2^20, then at most 1024 chunks
-  const int64_t short_ones = (n_pairs + 255) / 256 < 64 ? (n_pairs + 255) / 256 : 64;
-  const int64_t long_ones = (n_pairs + 1023) / 1024 < 1024 ? (n_pairs + 1023) / 1024 : 1024;
-  const int64_t chunks = short_ones > long_ones ? short_ones : long_ones;
-  return size_t(chunks > 0 ? chunks : 1) * size_t(n_experts) * sizeof(int32_t) + 256;
-}
-
 hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t stream) {
   const DispatchPlan p = plan_dispatch(a.n_tokens, a.n_experts, a.k, a.n_segments);
   if (p.nk == 0) {

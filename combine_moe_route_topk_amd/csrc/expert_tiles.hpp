@@ -140,6 +140,17 @@ __device__ __forceinline__ Tile direct_tile(int m, const int32_t* __restrict__ r
 struct GatherLayout {
   size_t counts, offsets, seg_offsets, dst_pos, order, dispatch_ws, total;
 };
+// The most that the dispatch of up to n_pairs pairs takes: fewer can take more chunks,
+// since a chunk's length jumps.  At most 64 of 256 pairs or more up to 65536 pairs, then
+// 1024 pairs each up to 2^20, then at most 1024 chunks.
+size_t most_dispatch_workspace(int64_t n_pairs, int n_experts) {
+  const int64_t even = (n_pairs + 255) / 256 < 64 ? (n_pairs + 255) / 256 : 64;
+  const int64_t longer = (n_pairs + 1023) / 1024 < 1024 ? (n_pairs + 1023) / 1024 : 1024;
+  const int64_t chunks = even > longer ? even : longer;
+  const size_t most = size_t(chunks) * size_t(n_experts) * 4 + 256;
+  const size_t own = dispatch_workspace_bytes(n_pairs, n_experts, 1, 1);
+  return most > own ? most : own;
+}
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 GatherLayout gather_layout(int64_t n_rows, int n_experts) {
   GatherLayout L{};
@@ -149,7 +160,7 @@ GatherLayout gather_layout(int64_t n_rows, int n_experts) {
   L.seg_offsets = o; o += round256(2 * 4);
   L.dst_pos = o;     o += round256(size_t(n_rows) * 4);
   L.order = o;       o += round256(size_t(n_rows) * 4);
-  L.dispatch_ws = o; o += round256(dispatch_workspace_bytes_up_to(n_rows, n_experts));
+  L.dispatch_ws = o; o += round256(most_dispatch_workspace(n_rows, n_experts));
   L.total = o;
   return L;
 }

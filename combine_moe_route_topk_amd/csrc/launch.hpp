@@ -34,9 +34,6 @@ struct DispatchPlan {
 
 DispatchPlan plan_dispatch(int64_t n_tokens, int n_experts, int k, int n_segments);
 size_t dispatch_workspace_bytes(int64_t n_tokens, int n_experts, int k, int n_segments);
-// No less than that of any dispatch of up to n_pairs pairs: fewer can take more
-// chunks, since a chunk's length jumps.
-size_t dispatch_workspace_bytes_up_to(int64_t n_pairs, int n_experts);
 
 struct DispatchArgs {
   const void* x;
