@@ -672,9 +672,9 @@ size_t moe_gather_gemm_int4_workspace_bytes(int64_t n_rows, int32_t n_experts);
  * rounded to y_dtype once.  Codes are multiplied exactly, a group's sum and the
  * sum over groups are fp32, in a fixed order.  silu as in moe_grouped_gemm_mxfp4
  * for a bf16 y, by the accurate exponential and a division for fp32.  A NaN scale
- * or bias makes its column's outputs NaN; a NaN or an infinity in a row makes the
- * row's outputs of g NaN or infinite, and no other row's.  Rows whose id lies
- * outside [0, E) leave y as it was.
+ * or bias makes its column's outputs NaN, an infinite one NaN or infinite; a NaN or
+ * an infinity in a row makes the row's outputs of g NaN or infinite, and no other
+ * row's.  Rows whose id lies outside [0, E) leave y as it was.
  *   rows        [n_rows, K] bfloat16, 16-byte aligned
  *   row_expert  [n_rows] int32, device-resident
  *   w, w_up     [E, N, K/2] codes, 16-byte aligned; w_up may be null

@@ -146,6 +146,22 @@ def test_nan_and_infinity_stay(name, affine):
             assert torch.isnan(got[hit]).all() and torch.equal(got[~hit], clean[~hit])
 
 
+@pytest.mark.parametrize("affine", [False, True])
+@pytest.mark.parametrize("name", SHAPES)
+def test_infinite_scales_and_biases_stay_in_their_column(name, affine):
+    r, e, k, n = _shape(name, 128, BF16, False)
+    case = _case(r, e, k, n, 128, affine, BF16, experts=_experts(r, e, skip=False))
+    clean = _call(case, BF16, F32)
+    hit = torch.zeros((r, n), dtype=torch.bool, device=DEV)
+    hit[to_dev(case[1] == 0), 7] = True
+    for part in (1, 2) if affine else (1,):
+        for group in (0, -1):
+            w = [v if v is None else v.copy() for v in case[2]]
+            w[part][0, 7, group] = np.inf
+            got = _call((case[0], case[1], tuple(w), None), BF16, F32)
+            assert not torch.isfinite(got[hit]).any() and torch.equal(got[~hit], clean[~hit])
+
+
 @pytest.mark.parametrize("glu", [False, True])
 @pytest.mark.parametrize("name", SHAPES)
 def test_replayed_and_on_two_streams(name, glu):
