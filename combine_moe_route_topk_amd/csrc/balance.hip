@@ -12,11 +12,11 @@
 // Both kernels read the logits once.  16 lanes hold a token of up to 256 experts
 // (a wave four tokens), so the row's maximum and sum are four exchanges within a
 // row of lanes; more experts take a whole wave per token.  A token's logits are
-// asked for while the one before it is worked on.  32768 tokens of 256 experts: 12.9
-// us forward (33.5 MB, 2.6 TB/s) and 8.4 us for the sums, 17.8 us backward (67 MB, 3.8
-// TB/s; a large copy reaches 4.95), with about 25 vector instructions to a logit, two
-// thirds of them the exponential's, which take some 7 us by themselves.  4096 tokens:
-// 4.1, 5.4 and 5.0 us, little more than launches and first loads.
+// asked for while the one before it is worked on.  32768 tokens of 256 experts in 37
+// sequences: 13.1 us forward (34.6 MB, 2.6 TB/s) and 8.7 us for the sums, 18.1 us backward
+// (67 MB, 3.7 TB/s; a large copy reaches 4.95), with 28 vector instructions to a logit
+// forward and 32 backward, two thirds of them the exponential's, which take some 7 us by
+// themselves.  4096 tokens: 4.1, 5.6 and 5.1 us, little more than launches and first loads.
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -326,7 +326,9 @@ constexpr int kDeep = 8;
 // LOOP: a workgroup per sequence takes all its experts, 32 after 32, and draws no
 // ticket, from kLoopBlocks workgroups of the other form on (each ticket makes a cache
 // visible to the other XCDs).  The whole loss of 4096 tokens of 256 experts in 64, 128
-// and 512 sequences, with tickets 21, 30 and 86 us, without 24, 25 and 27.
+// and 512 sequences, with tickets 21, 30 and 86 us, without 24, 25 and 27.  All of these
+// sequences are alike; the slots of one long sequence among many short ones are one
+// workgroup's too (32768 tokens in 128 sequences: 25 us, with one of 30000 tokens 61).
 constexpr int64_t kLoopBlocks = 768;
 template <bool VEC, bool LOOP>
 __global__ __launch_bounds__(kBlock) void balance_sum_kernel(ForwardArgs a, int n_slices) {

@@ -15,13 +15,13 @@
 // for B (-8 where there are no biases, which makes it the sum's start).
 //
 // Measured, bytes of codes, scales and biases over the time:
-//   1024 rows, 256 experts, K 7168, F 2048 SwiGLU, per 128:   671 us, 5.8 TB/s
-//   128 rows, 8 experts, K 4096, F 14336 SwiGLU, per 32 + b:  153 us, 3.8 TB/s
+//   1024 rows, 256 experts, K 7168, F 2048 SwiGLU, per 128:   654 us, 5.8 TB/s
+//   128 rows, 8 experts, K 4096, F 14336 SwiGLU, per 32 + b:  154 us, 3.8 TB/s
 //   48 rows, 8 experts, K 14336, N 4096, per 64, all fp32:     50 us, 5.3 TB/s
-//   8 rows, 8 of 256 experts, K 2048, N 7168, per 128:         14 us, 4.2 TB/s
-//   1 row, 1 expert, K 7168, N 2113, per 64 + b:               10 us, 0.85 TB/s
-// The first runs at the rate of memory (with the clocks that its power allows; 636
-// us on a cool card), the second at that of the vector units and LDS, which turn 4
+//   8 rows, 8 of 256 experts, K 2048, N 7168, per 128:         15 us, 4.1 TB/s
+//   1 row, 1 expert, K 7168, N 2113, per 64 + b:               11 us, 0.8 TB/s
+// The first runs at the rate of memory (with the clocks that its power allows: 636 to
+// 728 us), the second at that of the vector units and LDS, which turn 4
 // bits into bf16, scale every 32 elements and serve two row blocks; the last two are
 // one start, a chain of loads and one end, with 29 and 9 KB to read for a workgroup.
 #include <type_traits>

@@ -28,8 +28,8 @@ constexpr int kBlock = 256;
 // (256 MB).  Measured on 114688 x 4096 bf16, groups of 128, quantising with 1, 2 and
 // 4 octets: 237, 189 and 193 us (1.18 GB, 6.2 TB/s); back to bf16 with 1, 2, 4 and 8:
 // 226, 161, 165 and 166 (7.2 TB/s).  With ordinary loads quantising took 222 us.  (The
-// rounding below then took more instructions; with 2 octets it is 181 us now, 6.5 TB/s.)
-// 2113 x 7168 fp32 with biases per 32: 13.2 and 7.8 us (the launches and the groups'
+// rounding below then took more instructions; with 2 octets it is 177 us now, 6.7 TB/s.)
+// 2113 x 7168 fp32 with biases per 32: 13.5 and 7.8 us (the launches and the groups'
 // exchanges; 71 MB of x would take 9).
 constexpr int kQuant = 2, kDequant = 4;
 constexpr int64_t kCacheBytes = int64_t(256) << 20;
